@@ -344,6 +344,144 @@ HSA_API hsa_status_t hsa_backward(const hsa_problem_t *p, const void *Q, const v
                                   const int32_t *keff, const void *dO, float *dQ, float *dK, float *dV,
                                   float *dW_L, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Local attention beside the sparse one.  HSA reaches complete, strictly past chunks only (a query
+ * never sees its own chunk) and carries no positions.  A model built on it therefore pairs it with
+ * layers that attend to the recent tokens and to a few first ones, with rotary positions.  These
+ * calls are those layers: rotary positions, sliding-window attention with sinks and its backward,
+ * and a paged cache of ragged sequences (append, attention of the new tokens).
+ *
+ * Shared by these calls, beyond the conventions at the top:
+ *   - Visibility: the query at position p sees key u iff u <= p, u is cached, and
+ *     (window == 0, or p - u < window, or u < sinks).  A row that sees no key outputs zeros.
+ *   - d in {64, 128}; H % Hkv == 0, G = H / Hkv <= 16; B <= 65535; positions below 2^30.
+ *   - Values of keys that no query of the call sees (past the cached length, behind the window)
+ *     may be anything, NaN included; they are never used.  Other inputs are assumed finite.
+ *   - The status word at the start of the workspace is STICKY here: these calls never clear it (no
+ *     extra launch in a decode step), they only add to it.  Zero the workspace's first 256 bytes
+ *     once; hsa_get_device_status() reads and clears it and so reports on all calls since.
+ */
+typedef struct {
+    int32_t B, Tq, Tkv, H, Hkv, d;
+    int64_t q_pos0;      /* absolute position of query row 0 */
+    int32_t window;      /* tokens a query sees, itself included; 0 = all */
+    int32_t sinks;       /* first tokens that stay visible */
+    float scale;         /* on q . k; 0 = 1/sqrt(d) */
+    int32_t dtype;       /* hsa_dtype_t */
+    uint32_t flags;      /* HSA_FLAG_SIMT */
+    int32_t kv_cap;      /* Tcap: tokens per sequence the K/V buffers hold (0 = Tkv; else >= Tkv) */
+} hsa_window_t;
+
+/*
+ * Sliding-window attention with sinks, for whole prompts (Tq = Tkv, q_pos0 = 0), chunks of new
+ * tokens and single ones (q_pos0 = Tkv - Tq):
+ *   O[b][t][h][:] = sum_u P[u] V[b][u][j][:],  P = softmax over the visible keys of scale q . K[b][u][j][:]
+ * Q, O [B][Tq][H][d], K, V [B][Tcap][Hkv][d].  lse (NULL, or [B][Tq][H] fp32): the natural logarithm
+ * of sum_u exp(scale q . K[u]), -inf where no key is visible; hsa_window_backward needs it.
+ * bf16 rounds the probabilities to bf16 before the product with V (fp32 sums); fp32 and HSA_FLAG_SIMT
+ * keep fp32 throughout.  The sums' order depends on the sizes only: equal calls give equal bits.
+ */
+HSA_API hsa_status_t hsa_window_workspace_size(const hsa_window_t *p, size_t *bytes);
+HSA_API hsa_status_t hsa_window_attend(const hsa_window_t *p, const void *Q, const void *K, const void *V, void *O,
+                                       float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of hsa_window_attend with respect to Q, K and V for the upstream dO:
+ *   D = sum(dO o O);  P = exp(scale q . k - lse);  dS = P o (dO . v - D)
+ *   dV = sum P dO,  dQ = scale sum dS k,  dK = scale sum dS q   (dK, dV over all G heads of the group)
+ * in the problem's dtype, rounded once from fp32 sums and OVERWRITTEN: dQ [B][Tq][H][d], dK and dV
+ * [B][Tcap][Hkv][d] (zeros for tokens that no query sees).  O and lse as hsa_window_attend returned
+ * them.  bf16 rounds P and dS to bf16 before their products.  No atomics: equal calls give equal bits.
+ */
+HSA_API hsa_status_t hsa_window_backward_workspace_size(const hsa_window_t *p, size_t *bytes);
+HSA_API hsa_status_t hsa_window_backward(const hsa_window_t *p, const void *Q, const void *K, const void *V,
+                                         const void *O, const float *lse, const void *dO, void *dQ, void *dK,
+                                         void *dV, void *ws, size_t ws_bytes, void *stream);
+
+/* How the angles of a rotary embedding are scaled beyond the trained length (f_i = theta^(-2i/rot)). */
+typedef enum {
+    HSA_ROPE_NONE = 0,
+    HSA_ROPE_LINEAR = 1,   /* f_i / factor */
+    HSA_ROPE_NTK = 2,      /* theta * factor^(rot / (rot - 2)) in place of theta */
+    HSA_ROPE_YARN = 3,     /* by turns within orig_len: below `low` turns f_i / factor, above `high` f_i, a ramp
+                              over the pair index between; the rotated part times 0.1 ln(factor) + 1 */
+    HSA_ROPE_BANDS = 4     /* by turns n_i = orig_len f_i / 2 pi: n < low: f_i / factor; n > high: f_i; between
+                              (1 - u) f_i / factor + u f_i with u = (n - low) / (high - low) */
+} hsa_rope_scaling_t;
+
+typedef struct {
+    int32_t rot;           /* leading elements of each head that are rotated: even, 2 .. 128 */
+    int32_t interleaved;   /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1) */
+    int32_t scaling;       /* hsa_rope_scaling_t */
+    int32_t orig_len;      /* trained length (YARN, BANDS) */
+    double theta, factor;  /* factor >= 1 */
+    double low, high;      /* turns; both 0 = 1 and 32 (YARN), 1 and 4 (BANDS) */
+    double mscale;         /* factor on the rotated part; 0 = the scaling's own (1 unless YARN) */
+    double inv_freq[64];   /* written by hsa_rope_init */
+    double mult;           /* written by hsa_rope_init */
+} hsa_rope_t;
+
+/* Checks the fields above inv_freq and fills in inv_freq and mult (host only; once per model). */
+HSA_API hsa_status_t hsa_rope_init(hsa_rope_t *rope);
+
+/*
+ * Rotary positions of Q [B][Tq][H][d] and K [B][Tq][Hkv][d] in one launch (either may be NULL):
+ *   a = pos * inv_freq[i];  y1 = mult (x1 cos a - x2 sin a),  y2 = mult (x2 cos a + x1 sin a)
+ * for each pair of the first rot elements, the others copied.  Token t of sequence b sits at
+ * pos[b][t] (int32, device) or, with pos NULL, at q_pos0 + t.  The angle is taken in fp64 and reduced
+ * to one turn before its fp32 sine, so positions of millions keep their accuracy.  inverse != 0
+ * applies the transpose (-sin), which is the gradient's rotation.  Qr may be Q and Kr may be K;
+ * other overlaps are not allowed.  Of *p: B, Tq, H, Hkv, d, q_pos0, dtype.  No workspace.
+ */
+HSA_API hsa_status_t hsa_rope(const hsa_rope_t *rope, const hsa_window_t *p, const int32_t *pos, int inverse,
+                              const void *Q, const void *K, void *Qr, void *Kr, void *stream);
+
+/*
+ * A paged cache: K and V pages [npages][page][Hkv][d]; token u of sequence b lives in page
+ * table[b][u / page] at u % page.  The new tokens of all sequences lie back to back: sequence b owns
+ * rows q_start[b] .. q_start[b + 1] - 1 of the row tensors (n_b of them, 0 allowed), and kv_len[b]
+ * counts its cached tokens with the new ones, so its row i sits at position kv_len[b] - n_b + i.
+ * q_start [B + 1], kv_len [B] and table [B][max_pages] are int32 on the DEVICE: a captured graph can be
+ * replayed as they change, within the host-side bounds below.
+ */
+typedef struct {
+    int32_t B;
+    int32_t rows;        /* rows of the row tensors (>= q_start[B]; the ones behind are left as they are) */
+    int32_t max_q;       /* most new tokens of one sequence (0 = rows) */
+    int32_t max_kv;      /* most cached tokens of one sequence (0 = max_pages * page) */
+    int32_t H, Hkv, d;
+    int32_t page;        /* tokens per page: 16, 32, 64 or 128 */
+    int32_t npages;      /* pages in the pool */
+    int32_t max_pages;   /* row length of table */
+    int32_t window, sinks;
+    float scale;         /* as in hsa_window_t */
+    int32_t dtype;
+    uint32_t flags;      /* HSA_FLAG_SIMT */
+} hsa_paged_t;
+
+/*
+ * Writes the new tokens' K and V (k_new, v_new [rows][Hkv][d]) into their pages, K rotated on the
+ * way when rope is given, and, when Q is given, writes the rotated (or, without rope, copied)
+ * Q [rows][H][d] to Qr (Qr may be Q).  One launch.  A page number outside [0, npages) or a length
+ * outside its bounds is not followed: that write is skipped and recorded in the status word.
+ */
+HSA_API hsa_status_t hsa_paged_append(const hsa_paged_t *p, const hsa_rope_t *rope, const void *k_new,
+                                      const void *v_new, const void *Q, void *Qr, const int32_t *q_start,
+                                      const int32_t *kv_len, const int32_t *table, void *Kp, void *Vp, void *ws,
+                                      size_t ws_bytes, void *stream);
+
+/*
+ * Attention of the new tokens over the pages (chunked prefill, single tokens, both in one batch),
+ * with the visibility above.  Q, O [rows][H][d].  Pages wholly behind every query's window are never
+ * read: their table entries may be stale.  A page number outside [0, npages) where a key is visible
+ * reads as zero keys and values, and a length outside its bounds is cut to them; both are recorded in
+ * the status word (HSA_ERR_INVALID_ARG).
+ */
+HSA_API hsa_status_t hsa_paged_workspace_size(const hsa_paged_t *p, size_t *bytes);
+HSA_API hsa_status_t hsa_paged_attend(const hsa_paged_t *p, const void *Q, const void *Kp, const void *Vp,
+                                      const int32_t *q_start, const int32_t *kv_len, const int32_t *table, void *O,
+                                      void *ws, size_t ws_bytes, void *stream);
+
 /*
  * Synchronises `stream`, then reads and clears the device-status word in the
  * workspace header.  Every call that takes a workspace clears that word when it

@@ -19,11 +19,14 @@ import torch
 
 from . import _native
 from ._native import HSAError, hsa_problem_t
+from .local import (make_rope, paged_append, paged_attend, paged_workspace, rope, window_attend, window_backward,
+                    window_workspace)
 
 __all__ = ["make_problem", "plan", "workspace_size", "alloc_workspace", "landmarks", "landmarks_refined",
            "quest_summaries", "select", "select_noalloc", "attend", "forward", "forward_host",
            "forward_host_bytes", "decode_append", "attend_partials", "merge_partials", "device_status", "HSAError",
-           "hsa_problem_t", "kmax_of", "backward", "backward_workspace_size"]
+           "hsa_problem_t", "kmax_of", "backward", "backward_workspace_size", "make_rope", "rope", "window_workspace",
+           "window_attend", "window_backward", "paged_workspace", "paged_append", "paged_attend"]
 
 _DT = {torch.float32: _native.HSA_F32, torch.bfloat16: _native.HSA_BF16}
 

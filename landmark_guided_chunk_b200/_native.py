@@ -25,7 +25,9 @@ EXPORTED = ("hsa_workspace_size", "hsa_landmarks", "hsa_select", "hsa_attend", "
             "hsa_get_device_status", "hsa_plan", "hsa_status_string", "hsa_last_error", "hsa_abi_version",
             "hsa_select_noalloc", "hsa_decode_append", "hsa_attend_partials", "hsa_merge_partials",
             "hsa_backward_workspace_size", "hsa_backward", "hsa_noalloc_status", "hsa_landmarks_refined",
-            "hsa_debug_checks", "hsa_forward_host_bytes", "hsa_forward_host")
+            "hsa_debug_checks", "hsa_forward_host_bytes", "hsa_forward_host", "hsa_window_workspace_size",
+            "hsa_window_attend", "hsa_window_backward_workspace_size", "hsa_window_backward", "hsa_rope_init",
+            "hsa_rope", "hsa_paged_append", "hsa_paged_workspace_size", "hsa_paged_attend")
 PATH_NAMES = {0: "none", 1: "simt_rows", 2: "simt_split", 3: "tensor", 4: "mma_split"}
 
 
@@ -42,6 +44,28 @@ class hsa_plan_t(ctypes.Structure):
                 ("attend_path", ctypes.c_int32), ("landmark_kernels", ctypes.c_int32),
                 ("select_kernels", ctypes.c_int32), ("attend_kernels", ctypes.c_int32),
                 ("forward_fused", ctypes.c_int32)]
+
+
+class hsa_window_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Tq", ctypes.c_int32), ("Tkv", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("q_pos0", ctypes.c_int64),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("kv_cap", ctypes.c_int32)]
+
+
+class hsa_rope_t(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("orig_len", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("mscale", ctypes.c_double),
+                ("inv_freq", ctypes.c_double * 64), ("mult", ctypes.c_double)]
+
+
+class hsa_paged_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("npages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class HSAError(RuntimeError):
@@ -81,6 +105,17 @@ def lib() -> ctypes.CDLL:
     L.hsa_landmarks_refined.argtypes = [prob, P, P, P, P, P, P, P]
     L.hsa_backward_workspace_size.argtypes = [prob, ctypes.POINTER(ctypes.c_size_t)]
     L.hsa_backward.argtypes = [prob, P, P, P, P, P, I32p, Fp, I32p, P, Fp, Fp, Fp, Fp, P, Z, P]
+    win, rope, pag = (ctypes.POINTER(t) for t in (hsa_window_t, hsa_rope_t, hsa_paged_t))
+    size = ctypes.POINTER(ctypes.c_size_t)
+    L.hsa_window_workspace_size.argtypes = [win, size]
+    L.hsa_window_attend.argtypes = [win, P, P, P, P, Fp, P, Z, P]
+    L.hsa_window_backward_workspace_size.argtypes = [win, size]
+    L.hsa_window_backward.argtypes = [win, P, P, P, P, Fp, P, P, P, P, P, Z, P]
+    L.hsa_rope_init.argtypes = [rope]
+    L.hsa_rope.argtypes = [rope, win, I32p, ctypes.c_int, P, P, P, P, P]
+    L.hsa_paged_append.argtypes = [pag, rope, P, P, P, P, I32p, I32p, I32p, P, P, P, Z, P]
+    L.hsa_paged_workspace_size.argtypes = [pag, size]
+    L.hsa_paged_attend.argtypes = [pag, P, P, P, I32p, I32p, I32p, P, P, Z, P]
     L.hsa_status_string.argtypes = [ctypes.c_int]
     L.hsa_status_string.restype = ctypes.c_char_p
     L.hsa_last_error.argtypes = []
@@ -92,7 +127,10 @@ def lib() -> ctypes.CDLL:
     for f in ("hsa_workspace_size", "hsa_landmarks", "hsa_select", "hsa_attend", "hsa_forward",
               "hsa_get_device_status", "hsa_plan", "hsa_select_noalloc", "hsa_decode_append",
               "hsa_attend_partials", "hsa_merge_partials", "hsa_backward_workspace_size", "hsa_backward",
-              "hsa_noalloc_status", "hsa_landmarks_refined", "hsa_forward_host_bytes", "hsa_forward_host"):
+              "hsa_noalloc_status", "hsa_landmarks_refined", "hsa_forward_host_bytes", "hsa_forward_host",
+              "hsa_window_workspace_size", "hsa_window_attend", "hsa_window_backward_workspace_size",
+              "hsa_window_backward", "hsa_rope_init", "hsa_rope", "hsa_paged_append", "hsa_paged_workspace_size",
+              "hsa_paged_attend"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L

@@ -5,21 +5,12 @@
 #include <stdarg.h>
 #include <stdio.h>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api_util.cuh"
 #include "common.cuh"
 
 namespace hsa {
 
 static thread_local char g_err[512] = "";
-
-// An NVTX range around each launching entry point, named after it, so that a
-// timeline (nsys, ncu's range filters) shows the library's calls.  Header-only
-// NVTX: without an attached tool a range costs a null check.
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-};
 
 hsa_status_t fail(hsa_status_t s, const char *fmt, ...) {
     va_list ap;
@@ -193,12 +184,6 @@ hsa_status_t need(const void *x, bool required, const char *name) {
     if (!aligned16(x)) return fail(HSA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
     return HSA_OK;
 }
-
-#define HSA_TRY(expr)                       \
-    do {                                    \
-        hsa_status_t s_ = (expr);           \
-        if (s_ != HSA_OK) return s_;        \
-    } while (0)
 
 static hsa_status_t check_ws(const WsLayout &w, void *ws, size_t ws_bytes) {
     if (ws_bytes < w.total) return fail(HSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, w.total);
@@ -608,7 +593,7 @@ hsa_status_t hsa_get_device_status(void *ws, size_t ws_bytes, void *stream) {
         return fail(HSA_ERR_CUDA, "device-status word 0x%x: a kernel's internal index check failed (the access was "
                     "skipped or, in the debug build, clamped; results of that call are incomplete)", word);
     return fail(HSA_ERR_INVALID_ARG, "device-status word 0x%x: hsa_attend got a keff or chunk index outside "
-                "its row's candidates (those slots were skipped)", word);
+                "its row's candidates, or a paged call a page number or length outside its bounds (skipped)", word);
 }
 
 }  // extern "C"

@@ -1,0 +1,161 @@
+// local.cuh -- shared pieces of the local attention (sliding window with
+// sinks, contiguous or paged K/V): the kernels' view of a call, the geometry of
+// its visibility mask in key tiles, and the internal launch interface.
+#pragma once
+
+#include "common.cuh"
+
+namespace hsa {
+namespace local {
+
+// One call of hsa_window_attend or hsa_paged_attend as the kernels see it.
+// Rows are (token, head of the group) pairs of one kv head; tokens of all
+// sequences are numbered row0(b) + t.
+struct LocArgs {
+    int B, H, Hkv, G, d;
+    int max_q;             // most new tokens of one sequence (contiguous: Tq)
+    int max_kv;            // most cached tokens of one sequence (contiguous: Tkv)
+    int rows;              // tokens in Q / O over all sequences
+    int Tcap;              // contiguous: K/V tokens per sequence
+    int q_pos0;            // contiguous: position of row 0
+    int window;            // INT32_MAX = none
+    int sinks;
+    float scale, scale_log2;
+    int paged, page_shift, npages, max_pages;
+    const int32_t *q_start, *kv_len, *table;
+    int nsplit;            // key-axis splits per (sequence, kv head, row tile)
+    float *opart, *lpart;  // split partials: [nsplit][rows][H][d] and [nsplit][rows][H]
+    float *lse;            // optional output
+    uint32_t *status;
+};
+
+// One sequence of the call.
+struct Seq {
+    int row0, n;    // its tokens in Q / O
+    int pos0, kv;   // position of its first token (may be negative), cached tokens
+};
+
+__device__ __forceinline__ Seq seq_of(const LocArgs &a, int b) {
+    Seq s;
+    if (!a.paged) {
+        s.row0 = b * a.max_q;
+        s.n = a.max_q;
+        s.pos0 = a.q_pos0;
+        s.kv = a.max_kv;
+        return s;
+    }
+    // lengths are device data: anything outside the call's bounds is cut to them and recorded
+    const int r0 = a.q_start[b], r1 = a.q_start[b + 1], kv = a.kv_len[b];
+    s.row0 = min(max(r0, 0), a.rows);
+    const int r1c = min(max(r1, s.row0), a.rows);
+    s.n = min(r1c - s.row0, a.max_q);
+    s.kv = min(max(kv, 0), a.max_kv);
+    s.pos0 = s.kv - s.n;
+    if (threadIdx.x == 0 && (s.row0 != r0 || s.row0 + s.n != r1 || s.kv != kv)) atomicOr(a.status, DEV_BAD_INDEX);
+    return s;
+}
+
+// Row of the K/V tensors (in tokens) that holds token u of sequence b, or -1
+// if its page number is outside the pool.
+__device__ __forceinline__ long long kv_row(const LocArgs &a, int b, int u) {
+    if (!a.paged) return (long long)b * a.Tcap + u;
+    const int pg = a.table[(long long)b * a.max_pages + (u >> a.page_shift)];
+    if ((unsigned)pg >= (unsigned)a.npages) {
+        atomicOr(a.status, DEV_BAD_INDEX);
+        return -1;
+    }
+    return ((long long)pg << a.page_shift) + (u & ((1 << a.page_shift) - 1));
+}
+
+__host__ __device__ __forceinline__ bool visible(int p, int u, int kv, int window, int sinks) {
+    return u <= p && u < kv && (p - u < window || u < sinks);
+}
+
+// The key tiles (BK keys each, aligned to BK) that the queries at positions
+// pa .. pb reach: first those that only hold sinks, then the window's.
+struct Tiles {
+    int lo, hi;       // window keys [lo, hi)
+    int ns;           // sink keys [0, ns) before the window (ns <= lo)
+    int nst, wt0, nt; // tiles of the sinks, first window tile, tiles in all
+    __host__ __device__ __forceinline__ int tile(int i) const { return i < nst ? i : wt0 + i - nst; }
+};
+
+template <int BK> __host__ __device__ __forceinline__ Tiles tiles_of(int pa, int pb, int kv, int window, int sinks) {
+    Tiles t;
+    t.hi = pb + 1 < kv ? pb + 1 : kv;
+    if (t.hi < 0) t.hi = 0;
+    t.lo = pa >= window ? pa - window + 1 : 0;   // window may be INT32_MAX
+    if (t.lo > t.hi) t.lo = t.hi;
+    t.ns = sinks < t.lo ? sinks : t.lo;
+    t.wt0 = t.lo / BK;
+    const int wt1 = t.hi > t.lo ? (t.hi + BK - 1) / BK : t.wt0;
+    t.nst = (t.ns + BK - 1) / BK;
+    if (t.hi > t.lo && t.nst > t.wt0) t.nst = t.wt0;   // the first window tile holds the last sinks too
+    t.nt = t.nst + wt1 - t.wt0;
+    return t;
+}
+
+// Keys of tile [u0, u0 + BK) that some query of the block sees lie in [a, b) or below ns.
+// (Others are loaded as zeros: nothing of theirs reaches a sum, NaN included.)
+__host__ __device__ __forceinline__ bool key_live(const Tiles &t, int u) { return u < t.hi && (u >= t.lo || u < t.ns); }
+
+// True if every query at pa .. pb sees every key u0 .. u0 + n - 1 (no mask needed).
+__host__ __device__ __forceinline__ bool tile_full(int pa, int pb, int u0, int n, int kv, int window, int sinks) {
+    const int ul = u0 + n - 1;
+    return ul <= pa && ul < kv && (pb - u0 < window || ul < sinks);
+}
+
+// Split s of the nt tiles: [i0, i1).
+__host__ __device__ __forceinline__ void split_range(int nt, int nsplit, int s, int *i0, int *i1) {
+    const int per = (nt + nsplit - 1) / nsplit;
+    *i0 = s * per < nt ? s * per : nt;
+    *i1 = *i0 + per < nt ? *i0 + per : nt;
+}
+
+// Backward: the key tiles that hold sinks are seen by every later query.  Their
+// far part (queries beyond the window) is cut into chunks of `far_q` tokens, each
+// a work item of its own that writes fp32 partials.
+struct BwdArgs {
+    LocArgs a;                       // contiguous view; a.lse = the forward's
+    int nkt;                         // key tiles over Tkv
+    int nst;                         // key tiles that hold sinks and have a far part (0: none)
+    int nfar, far_q;                 // far chunks per such tile, tokens per chunk
+    float *D;                        // [B][Tq][H] row sums of dO o O
+    float *part;                     // [2 (dK, dV)][nfar + 1][B][Hkv][nst * BK][d]
+};
+
+struct LocPlan {
+    bool tc, few;          // forward path: tcgen05 tiles, few-row kernel; neither: CUDA-core tiles
+    int nsplit;
+    size_t opart, lpart, total;
+};
+LocPlan plan_forward(const LocArgs &a, int dtype, bool simt);
+
+struct BwdPlan {
+    bool tc;
+    int nkt, nst, nfar, far_q, bk;
+    size_t D, part, extra, total;
+};
+BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt);
+
+cudaError_t launch_simt(const LocArgs &a, int dtype, const void *Q, const void *K, const void *V, void *O,
+                        cudaStream_t st);
+cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st);
+cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st);
+cudaError_t launch_bwd_simt(const BwdArgs &w, int dtype, const void *Q, const void *K, const void *V, const void *dO,
+                            void *dQ, void *dK, void *dV, cudaStream_t st);
+cudaError_t launch_bwd_join(const BwdArgs &w, int bk, int dtype, void *dK, void *dV, cudaStream_t st);
+
+struct RopeArgs {
+    double f[64];
+    float mult;
+    int rot, interleaved;
+    float sgn;             // +1 forward, -1 transpose
+};
+cudaError_t launch_rope(const RopeArgs &r, int dtype, int B, int T, int H, int Hkv, int d, int pos0,
+                        const int32_t *pos, const void *Q, const void *K, void *Qr, void *Kr, cudaStream_t st);
+cudaError_t launch_append(const RopeArgs *r, const LocArgs &a, int dtype, const void *k, const void *v, const void *Q,
+                          void *Qr, void *Kp, void *Vp, cudaStream_t st);
+
+}  // namespace local
+}  // namespace hsa

@@ -1,0 +1,561 @@
+// window_simt.cu -- sliding-window attention with sinks on the CUDA cores, in
+// fp32 throughout: the fp32 problems' kernels, and the ones HSA_FLAG_SIMT asks
+// for.  Contiguous or paged K/V.  Also the pieces every path shares: the join
+// of key-axis splits, the row sums D of the backward, and the join of the
+// backward's far-sink partials.
+#include "local.cuh"
+
+namespace hsa {
+namespace local {
+
+namespace {
+
+constexpr int BM = 64;   // rows (token, head) per CTA
+constexpr int BN = 64;   // keys per tile
+constexpr int NT = 256;  // 16 x 16 threads: 4 rows x 4 keys of S each
+constexpr int PP = BN + 4;
+
+// Rows r0 .. r0+63 of a [rows][stride] tensor into shared memory as fp32 (pitch P);
+// row r is read at src(r), or zero where that is negative.
+template <typename T, int D, int P, typename Src>
+__device__ __forceinline__ void load_rows(float *dst, const T *__restrict__ g, Src src) {
+    constexpr int V = 16 / sizeof(T);    // elements per 16-byte load
+    constexpr int PR = D / V;            // loads per row
+    for (int i = threadIdx.x; i < 64 * PR; i += NT) {
+        const int r = i / PR, c = (i % PR) * V;
+        const long long at = src(r);
+        float f[V];
+        if (at >= 0) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(g + at + c);
+            const T *t = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int x = 0; x < V; ++x) f[x] = to_f32(t[x]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < V; ++x) f[x] = 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < V; x += 4)
+            *reinterpret_cast<float4 *>(dst + r * P + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+    }
+}
+
+// s[i][j] = row (ty*4 + i) of A . row (tx + 16 j) of B, over D
+template <int D, int PA, int PB>
+__device__ __forceinline__ void dot_tile(const float *A, const float *B, int ty, int tx, float (&s)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < D; x += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (ty * 4 + i) * PA + x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * PB + x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+            }
+    }
+}
+
+// acc[i][c] += sum_k P[row ty*4 + i][k] X[k][col], columns tx*4 + 64*(c/4) + c%4.
+// PT: P is stored [k][row] instead (transposed product).
+template <int D, int PX, bool PT>
+__device__ __forceinline__ void acc_tile(const float *Pm, const float *X, int ty, int tx, float (&acc)[4][D / 16]) {
+#pragma unroll 4
+    for (int k = 0; k < 64; ++k) {
+        float p[4];
+        if (PT) {
+            const float4 v = *reinterpret_cast<const float4 *>(Pm + k * PP + ty * 4);
+            p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = Pm[(ty * 4 + i) * PP + k];
+        }
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float4 v = *reinterpret_cast<const float4 *>(X + k * PX + tx * 4 + 64 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][4 * c + 0] = fmaf(p[i], v.x, acc[i][4 * c + 0]);
+                acc[i][4 * c + 1] = fmaf(p[i], v.y, acc[i][4 * c + 1]);
+                acc[i][4 * c + 2] = fmaf(p[i], v.z, acc[i][4 * c + 2]);
+                acc[i][4 * c + 3] = fmaf(p[i], v.w, acc[i][4 * c + 3]);
+            }
+        }
+    }
+}
+
+template <typename T> __device__ __forceinline__ void store4(T *p, float a, float b, float c, float d);
+template <> __device__ __forceinline__ void store4<float>(float *p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float a, float b, float c, float d) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    uint2 u;
+    u.x = *reinterpret_cast<uint32_t *>(&lo);
+    u.y = *reinterpret_cast<uint32_t *>(&hi);
+    *reinterpret_cast<uint2 *>(p) = u;
+}
+
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, o));
+    return x;
+}
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+    return x;
+}
+
+// Forward: one pass over the block's key tiles with a running maximum m and
+// sum l per row; O is rescaled by exp(m_old - m_new) when the maximum grows.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__restrict__ Q, const T *__restrict__ K,
+                                                      const T *__restrict__ V, T *__restrict__ O) {
+    extern __shared__ __align__(16) float sm[];
+    float *sQ = sm, *sK = sQ + BM * D, *sV = sK + BN * (D + 4), *sP = sV + BN * D;
+    const int b = blockIdx.z, j = blockIdx.y;
+    const int split = blockIdx.x % a.nsplit, blk = blockIdx.x / a.nsplit;
+    const int tok = BM / a.G;                       // tokens per block
+    const Seq s = seq_of(a, b);
+    const int t0 = blk * tok, t1 = min(s.n, t0 + tok);
+    if (t0 >= s.n) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const Tiles tl = tiles_of<BN>(s.pos0 + t0, s.pos0 + t1 - 1, s.kv, a.window, a.sinks);
+    int i0, i1;
+    split_range(tl.nt, a.nsplit, split, &i0, &i1);
+
+    load_rows<T, D, D>(sQ, Q, [&](int r) -> long long {
+        const int t = t0 + r / a.G;
+        return r < tok * a.G && t < t1 ? ((long long)(s.row0 + t) * a.H + j * a.G + r % a.G) * D : -1;
+    });
+    float m[4], l[4], o[4][D / 16];
+    int p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        p[i] = r < tok * a.G && t0 + r / a.G < t1 ? s.pos0 + t0 + r / a.G : -1;   // -1: sees nothing
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+    for (int it = i0; it < i1; ++it) {
+        const int u0 = tl.tile(it) * BN;
+        __syncthreads();
+        auto src = [&](int r) -> long long {
+            if (!key_live(tl, u0 + r)) return -1;
+            const long long row = kv_row(a, b, u0 + r);
+            return row < 0 ? -1 : (row * a.Hkv + j) * D;
+        };
+        load_rows<T, D, D + 4>(sK, K, src);
+        load_rows<T, D, D>(sV, V, src);
+        __syncthreads();
+        float sc[4][4];
+        dot_tile<D, D, D + 4>(sQ, sK, ty, tx, sc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int u = u0 + tx + 16 * c;
+                sc[i][c] = visible(p[i], u, s.kv, a.window, a.sinks) ? sc[i][c] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, sc[i][c]);
+            }
+            mx = fmaxf(m[i], max16(mx));
+            const float ref = mx == -INFINITY ? 0.f : mx;   // rows without a key so far: every exp is 0
+            const float f = exp2f(m[i] - ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float e = exp2f(sc[i][c] - ref);
+                sum += e;
+                sP[(ty * 4 + i) * PP + tx + 16 * c] = e;
+            }
+            l[i] = l[i] * f + sum16(sum);
+            m[i] = mx;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
+        }
+        __syncwarp();   // a warp reads only the P rows that it wrote
+        acc_tile<D, D, false>(sP, sV, ty, tx, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        if (r >= tok * a.G || t0 + r / a.G >= t1) continue;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const float lse = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
+        const long long row = (long long)(s.row0 + t0 + r / a.G) * a.H + j * a.G + r % a.G;
+        const long long prow = (long long)split * a.rows * a.H + row;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float x = o[i][4 * c] * inv, y = o[i][4 * c + 1] * inv, z = o[i][4 * c + 2] * inv,
+                        w = o[i][4 * c + 3] * inv;
+            if (a.nsplit > 1)
+                store4<float>(a.opart + prow * D + tx * 4 + 64 * c, x, y, z, w);
+            else
+                store4<T>(O + row * D + tx * 4 + 64 * c, x, y, z, w);
+        }
+        if (tx == 0) {
+            if (a.nsplit > 1)
+                a.lpart[prow] = lse;
+            else if (a.lse)
+                a.lse[row] = lse;
+        }
+    }
+}
+
+// Joins the key-axis splits of a row: O = sum_s exp(lse_s - lse) O_s with
+// lse = ln sum_s exp(lse_s), in split order.  One warp per (token, head).
+// Only the rows of the call's sequences were written; the others are left alone.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) combine_kernel(LocArgs a, T *__restrict__ O) {
+    const int b = blockIdx.y;
+    const Seq s = seq_of(a, b);
+    const int lane = threadIdx.x & 31;
+    const long long e = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (e >= (long long)s.n * a.H) return;
+    const long long row = (long long)s.row0 * a.H + e;
+    const long long stride = (long long)a.rows * a.H;
+    float mx = -INFINITY;
+    for (int i = lane; i < a.nsplit; i += 32) mx = fmaxf(mx, a.lpart[i * stride + row]);
+    mx = warp_max(mx);
+    constexpr int N = D / 32;
+    float acc[N], l = 0.f;
+#pragma unroll
+    for (int x = 0; x < N; ++x) acc[x] = 0.f;
+    if (mx != -INFINITY) {
+        for (int i = 0; i < a.nsplit; ++i) {
+            const float w = expf(a.lpart[i * stride + row] - mx);
+            l += w;
+            const float *src = a.opart + (i * stride + row) * D + lane * N;
+#pragma unroll
+            for (int x = 0; x < N; ++x) acc[x] = fmaf(w, src[x], acc[x]);
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int x = 0; x < N; ++x) O[row * D + lane * N + x] = from_f32<T>(acc[x] * inv);
+    if (lane == 0 && a.lse) a.lse[row] = l > 0.f ? mx + logf(l) : -INFINITY;
+}
+
+// D[row] = sum_x dO[row][x] O[row][x], one warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) rowdot_kernel(const T *__restrict__ O, const T *__restrict__ dO,
+                                                     float *__restrict__ out, long long n) {
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= n) return;
+    constexpr int N = D / 32;
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < N; ++x) s = fmaf(to_f32(O[row * D + lane * N + x]), to_f32(dO[row * D + lane * N + x]), s);
+    s = warp_sum(s);
+    if (lane == 0) out[row] = s;
+}
+
+// dQ: the forward's iteration; P from lse, dP = dO V^T, dS = P (dP - D), dQ += dS K.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restrict__ Q, const T *__restrict__ K,
+                                                     const T *__restrict__ V, const T *__restrict__ dO,
+                                                     T *__restrict__ dQ) {
+    extern __shared__ __align__(16) float sm[];
+    const LocArgs &a = w.a;
+    float *sQ = sm, *sG = sQ + BM * D, *sK = sG + BM * D, *sV = sK + BN * (D + 4), *sP = sV + BN * (D + 4);
+    const int b = blockIdx.z, j = blockIdx.y;
+    const int tok = BM / a.G;
+    const Seq s = seq_of(a, b);
+    const int t0 = blockIdx.x * tok, t1 = min(s.n, t0 + tok);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const Tiles tl = tiles_of<BN>(s.pos0 + t0, s.pos0 + t1 - 1, s.kv, a.window, a.sinks);
+    auto qsrc = [&](int r) -> long long {
+        const int t = t0 + r / a.G;
+        return r < tok * a.G && t < t1 ? ((long long)(s.row0 + t) * a.H + j * a.G + r % a.G) * D : -1;
+    };
+    load_rows<T, D, D>(sQ, Q, qsrc);
+    load_rows<T, D, D>(sG, dO, qsrc);
+    float lse2[4], dd[4], acc[4][D / 16];
+    int p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long at = qsrc(ty * 4 + i);
+        p[i] = at >= 0 ? s.pos0 + t0 + (ty * 4 + i) / a.G : -1;
+        lse2[i] = at >= 0 ? a.lse[at / D] * 1.4426950408889634f : 0.f;
+        dd[i] = at >= 0 ? w.D[at / D] : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+    }
+    for (int it = 0; it < tl.nt; ++it) {
+        const int u0 = tl.tile(it) * BN;
+        __syncthreads();
+        auto src = [&](int r) -> long long {
+            return key_live(tl, u0 + r) ? (kv_row(a, b, u0 + r) * a.Hkv + j) * D : -1;
+        };
+        load_rows<T, D, D + 4>(sK, K, src);
+        load_rows<T, D, D + 4>(sV, V, src);
+        __syncthreads();
+        float sc[4][4], dp[4][4];
+        dot_tile<D, D, D + 4>(sQ, sK, ty, tx, sc);
+        dot_tile<D, D, D + 4>(sG, sV, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bool vis = visible(p[i], u0 + tx + 16 * c, s.kv, a.window, a.sinks);
+                const float pr = vis ? exp2f(fmaf(sc[i][c], a.scale_log2, -lse2[i])) : 0.f;
+                sP[(ty * 4 + i) * PP + tx + 16 * c] = vis ? pr * (dp[i][c] - dd[i]) : 0.f;
+            }
+        __syncwarp();
+        acc_tile<D, D + 4, false>(sP, sK, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long at = qsrc(ty * 4 + i);
+        if (at < 0) continue;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            store4<T>(dQ + at + tx * 4 + 64 * c, acc[i][4 * c] * a.scale, acc[i][4 * c + 1] * a.scale,
+                      acc[i][4 * c + 2] * a.scale, acc[i][4 * c + 3] * a.scale);
+    }
+}
+
+// dK, dV of one key tile: over the rows of every query token that sees it.
+// Work item x: tiles 0 .. nkt-1 with the queries inside their window, then the
+// far chunks of the sink tiles (fp32 partials, joined by bwd_join_kernel).
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__restrict__ Q, const T *__restrict__ K,
+                                                      const T *__restrict__ V, const T *__restrict__ dO,
+                                                      T *__restrict__ dK, T *__restrict__ dV) {
+    extern __shared__ __align__(16) float sm[];
+    const LocArgs &a = w.a;
+    float *sK = sm, *sV = sK + BN * (D + 4), *sQ = sV + BN * (D + 4), *sG = sQ + BM * (D + 4),
+          *sP = sG + BM * (D + 4), *sS = sP + BM * PP;
+    const int b = blockIdx.z, j = blockIdx.y;
+    const Seq s = seq_of(a, b);
+    int kt = blockIdx.x, far = -1;
+    if (kt >= w.nkt) {
+        far = (kt - w.nkt) % w.nfar;
+        kt = (kt - w.nkt) / w.nfar;
+    }
+    const int u0 = kt * BN, ul = min(u0 + BN, s.kv) - 1;
+    const bool sink = kt < w.nst;
+    // query tokens [ta, tb): from the tile's first key on; inside the window of its last key, or the far chunk
+    int ta = max(0, u0 - s.pos0), tb = s.n;
+    if (a.window < INT32_MAX) {
+        const long long edge = (long long)ul + a.window - s.pos0;   // first token beyond the window of every key
+        if (far < 0)
+            tb = (int)max(0ll, min((long long)s.n, edge));
+        else {
+            const long long f0 = max(0ll, max((long long)ta, edge));
+            ta = (int)min((long long)s.n, f0 + (long long)far * w.far_q);
+            tb = (int)min((long long)s.n, f0 + (long long)(far + 1) * w.far_q);
+        }
+    }
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    auto src = [&](int r) -> long long {
+        return u0 + r < s.kv ? (kv_row(a, b, u0 + r) * a.Hkv + j) * D : -1;
+    };
+    const int tok = BM / a.G;
+    float gk[4][D / 16], gv[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) gk[i][c] = gv[i][c] = 0.f;
+    if (ta < tb) {
+        load_rows<T, D, D + 4>(sK, K, src);
+        load_rows<T, D, D + 4>(sV, V, src);
+    }
+    for (int t0 = ta; t0 < tb; t0 += tok) {
+        const int t1 = min(tb, t0 + tok);
+        auto qsrc = [&](int r) -> long long {
+            const int t = t0 + r / a.G;
+            return r < tok * a.G && t < t1 ? ((long long)(s.row0 + t) * a.H + j * a.G + r % a.G) * D : -1;
+        };
+        __syncthreads();
+        load_rows<T, D, D + 4>(sQ, Q, qsrc);
+        load_rows<T, D, D + 4>(sG, dO, qsrc);
+        __syncthreads();
+        float sc[4][4], dp[4][4];
+        dot_tile<D, D + 4, D + 4>(sQ, sK, ty, tx, sc);
+        dot_tile<D, D + 4, D + 4>(sG, sV, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            const long long at = qsrc(r);
+            const int p = at >= 0 ? s.pos0 + t0 + r / a.G : -1;
+            const float lse2 = at >= 0 ? a.lse[at / D] * 1.4426950408889634f : 0.f;
+            const float dd = at >= 0 ? w.D[at / D] : 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bool vis = visible(p, u0 + tx + 16 * c, s.kv, a.window, a.sinks);
+                const float pr = vis ? exp2f(fmaf(sc[i][c], a.scale_log2, -lse2)) : 0.f;
+                sP[r * PP + tx + 16 * c] = pr;
+                sS[r * PP + tx + 16 * c] = vis ? pr * (dp[i][c] - dd) : 0.f;
+            }
+        }
+        __syncthreads();
+        // key rows ty*4 + i: sum over the 64 query rows of P[row][key] dO[row][:]
+        acc_tile<D, D + 4, true>(sP, sG, ty, tx, gv);
+        acc_tile<D, D + 4, true>(sS, sQ, ty, tx, gk);
+    }
+    const long long psz = (long long)a.B * a.Hkv * w.nst * BN * D;   // one slot of partials
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int u = u0 + ty * 4 + i;
+        if (u >= s.kv) continue;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const int col = tx * 4 + 64 * c;
+            float k4[4], v4[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                k4[x] = gk[i][4 * c + x] * a.scale;
+                v4[x] = gv[i][4 * c + x];
+            }
+            if (sink) {
+                const long long at = (((long long)b * a.Hkv + j) * w.nst * BN + u) * D + col;
+                float *pk = w.part + (far + 1) * psz + at, *pv = pk + (w.nfar + 1) * psz;
+                store4<float>(pk, k4[0], k4[1], k4[2], k4[3]);
+                store4<float>(pv, v4[0], v4[1], v4[2], v4[3]);
+            } else {
+                const long long at = (((long long)b * a.Tcap + u) * a.Hkv + j) * D + col;
+                store4<T>(dK + at, k4[0], k4[1], k4[2], k4[3]);
+                store4<T>(dV + at, v4[0], v4[1], v4[2], v4[3]);
+            }
+        }
+    }
+}
+
+// dK, dV of the sink tiles: their partials summed in slot order (window part
+// first, then the far chunks), rounded once.  One thread per four elements.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) bwd_join_kernel(BwdArgs w, int bk, T *__restrict__ dK, T *__restrict__ dV) {
+    const LocArgs &a = w.a;
+    const long long psz = (long long)a.B * a.Hkv * w.nst * bk * D;
+    const long long e = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (e >= psz) return;
+    const int u = (int)(e / D % (w.nst * bk));
+    const long long bj = e / D / (w.nst * bk);
+    if (u >= a.max_kv) return;
+    const float *src = w.part + (blockIdx.y ? (w.nfar + 1) * psz : 0) + e;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i <= w.nfar; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(src + i * psz);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    T *dst = (blockIdx.y ? dV : dK) + ((bj / a.Hkv * a.Tcap + u) * a.Hkv + bj % a.Hkv) * D + e % D;
+    store4<T>(dst, s.x, s.y, s.z, s.w);
+}
+
+template <typename F> cudaError_t with_smem(F f, size_t bytes) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int D>
+cudaError_t fwd(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
+    const size_t smem = (BM * D + BN * (D + 4) + BN * D + BM * PP) * sizeof(float);
+    cudaError_t e = with_smem(simt_fwd_kernel<T, D>, smem);
+    if (e != cudaSuccess) return e;
+    const int tok = BM / a.G;
+    const dim3 grid((unsigned)((a.max_q + tok - 1) / tok) * a.nsplit, a.Hkv, a.B);
+    simt_fwd_kernel<T, D><<<grid, NT, smem, st>>>(a, (const T *)Q, (const T *)K, (const T *)V, (T *)O);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t bwd(const BwdArgs &w, const void *Q, const void *K, const void *V, const void *dO, void *dQ, void *dK,
+                void *dV, cudaStream_t st) {
+    const size_t s1 = (2 * BM * D + 2 * BN * (D + 4) + BM * PP) * sizeof(float);
+    const size_t s2 = (4 * BN * (D + 4) + 2 * BM * PP) * sizeof(float);
+    cudaError_t e = with_smem(simt_dq_kernel<T, D>, s1);
+    if (e == cudaSuccess) e = with_smem(simt_dkv_kernel<T, D>, s2);
+    if (e != cudaSuccess) return e;
+    const int tok = BM / w.a.G;
+    if (w.a.max_q > 0)
+        simt_dq_kernel<T, D><<<dim3((w.a.max_q + tok - 1) / tok, w.a.Hkv, w.a.B), NT, s1, st>>>(
+            w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dQ);
+    if (w.nkt > 0)
+        simt_dkv_kernel<T, D><<<dim3(w.nkt + w.nst * w.nfar, w.a.Hkv, w.a.B), NT, s2, st>>>(
+            w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dK, (T *)dV);
+    return cudaGetLastError();
+}
+
+#define BY_TYPE(call_f64, call_f128, call_b64, call_b128) \
+    (dtype == HSA_F32 ? (d == 64 ? call_f64 : call_f128) : (d == 64 ? call_b64 : call_b128))
+
+}  // namespace
+
+cudaError_t launch_simt(const LocArgs &a, int dtype, const void *Q, const void *K, const void *V, void *O,
+                        cudaStream_t st) {
+    const int d = a.d;
+    return BY_TYPE((fwd<float, 64>(a, Q, K, V, O, st)), (fwd<float, 128>(a, Q, K, V, O, st)),
+                   (fwd<__nv_bfloat16, 64>(a, Q, K, V, O, st)), (fwd<__nv_bfloat16, 128>(a, Q, K, V, O, st)));
+}
+
+cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st) {
+    const int d = a.d;
+    const dim3 grid((unsigned)(((long long)a.max_q * a.H + 7) / 8), a.B);
+    if (dtype == HSA_F32) {
+        if (d == 64) combine_kernel<float, 64><<<grid, 256, 0, st>>>(a, (float *)O);
+        else combine_kernel<float, 128><<<grid, 256, 0, st>>>(a, (float *)O);
+    } else {
+        if (d == 64) combine_kernel<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(a, (__nv_bfloat16 *)O);
+        else combine_kernel<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(a, (__nv_bfloat16 *)O);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st) {
+    const long long n = (long long)a.rows * a.H;
+    if (n == 0) return cudaSuccess;
+    const unsigned g = (unsigned)((n + 7) / 8);
+    if (dtype == HSA_F32) {
+        if (a.d == 64) rowdot_kernel<float, 64><<<g, 256, 0, st>>>((const float *)O, (const float *)dO, D, n);
+        else rowdot_kernel<float, 128><<<g, 256, 0, st>>>((const float *)O, (const float *)dO, D, n);
+    } else {
+        typedef __nv_bfloat16 h;
+        if (a.d == 64) rowdot_kernel<h, 64><<<g, 256, 0, st>>>((const h *)O, (const h *)dO, D, n);
+        else rowdot_kernel<h, 128><<<g, 256, 0, st>>>((const h *)O, (const h *)dO, D, n);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_simt(const BwdArgs &w, int dtype, const void *Q, const void *K, const void *V, const void *dO,
+                            void *dQ, void *dK, void *dV, cudaStream_t st) {
+    const int d = w.a.d;
+    return BY_TYPE((bwd<float, 64>(w, Q, K, V, dO, dQ, dK, dV, st)), (bwd<float, 128>(w, Q, K, V, dO, dQ, dK, dV, st)),
+                   (bwd<__nv_bfloat16, 64>(w, Q, K, V, dO, dQ, dK, dV, st)),
+                   (bwd<__nv_bfloat16, 128>(w, Q, K, V, dO, dQ, dK, dV, st)));
+}
+
+cudaError_t launch_bwd_join(const BwdArgs &w, int bk, int dtype, void *dK, void *dV, cudaStream_t st) {
+    if (w.nst == 0) return cudaSuccess;
+    const long long psz = (long long)w.a.B * w.a.Hkv * w.nst * bk * w.a.d;
+    const dim3 grid((unsigned)((psz / 4 + 255) / 256), 2);
+    if (dtype == HSA_F32) {
+        if (w.a.d == 64) bwd_join_kernel<float, 64><<<grid, 256, 0, st>>>(w, bk, (float *)dK, (float *)dV);
+        else bwd_join_kernel<float, 128><<<grid, 256, 0, st>>>(w, bk, (float *)dK, (float *)dV);
+    } else {
+        typedef __nv_bfloat16 h;
+        if (w.a.d == 64) bwd_join_kernel<h, 64><<<grid, 256, 0, st>>>(w, bk, (h *)dK, (h *)dV);
+        else bwd_join_kernel<h, 128><<<grid, 256, 0, st>>>(w, bk, (h *)dK, (h *)dV);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace local
+}  // namespace hsa

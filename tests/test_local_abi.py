@@ -1,0 +1,178 @@
+"""Local attention on the host: hsa_rope_init against its formulas, and every refusal of the
+entry points (an invalid call launches nothing, so no GPU is needed)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import landmark_guided_chunk_b200 as hsa
+from landmark_guided_chunk_b200 import _native
+from landmark_guided_chunk_b200._native import hsa_paged_t, hsa_rope_t, hsa_window_t
+from tests.local_ref import inv_freq
+
+INVALID, UNSUPPORTED, WORKSPACE = (_native.HSA_ERR_INVALID_ARG, _native.HSA_ERR_UNSUPPORTED,
+                                   _native.HSA_ERR_WORKSPACE)
+PTR = 1 << 20      # never followed: the calls below are refused first
+BIG = 1 << 60
+
+
+def _window(**kw):
+    base = dict(B=2, Tq=100, Tkv=100, H=8, Hkv=2, d=128, q_pos0=0, window=10, sinks=2, scale=0.0, dtype=1, flags=0,
+                kv_cap=0)
+    base.update(kw)
+    return hsa_window_t(**base)
+
+
+def _paged(**kw):
+    base = dict(B=2, rows=10, max_q=5, max_kv=0, H=8, Hkv=2, d=128, page=16, npages=9, max_pages=4, window=0, sinks=0,
+                scale=0.0, dtype=1, flags=0)
+    base.update(kw)
+    return hsa_paged_t(**base)
+
+
+COMMON = [(dict(H=7), INVALID), (dict(H=0), INVALID), (dict(Hkv=0), INVALID), (dict(B=-1), INVALID),
+          (dict(dtype=2), INVALID), (dict(flags=1), INVALID), (dict(flags=64), INVALID),
+          (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
+          (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED),
+          (dict(H=34), UNSUPPORTED), (dict(B=65536), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(Tq=-1), INVALID), (dict(Tkv=-1), INVALID), (dict(q_pos0=-1), INVALID), (dict(kv_cap=99), INVALID),
+    (dict(q_pos0=1 << 30), UNSUPPORTED), (dict(q_pos0=1 << 40), UNSUPPORTED), (dict(kv_cap=(1 << 30) + 1), UNSUPPORTED),
+    (dict(B=2048, kv_cap=1 << 20), UNSUPPORTED), (dict(B=2048, Tq=1 << 20), UNSUPPORTED)])
+def test_window_refusals(kw, status):
+    L = _native.lib()
+    n = ctypes.c_size_t(77)
+    p = ctypes.byref(_window(**kw))
+    assert L.hsa_window_workspace_size(p, ctypes.byref(n)) == status
+    assert L.hsa_window_backward_workspace_size(p, ctypes.byref(n)) == status
+    assert n.value == 77 and L.hsa_last_error()
+    assert L.hsa_window_attend(p, PTR, PTR, PTR, PTR, None, PTR, BIG, None) == status
+    assert L.hsa_window_backward(p, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, BIG, None) == status
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(rows=-1), INVALID), (dict(max_q=-1), INVALID), (dict(max_kv=-1), INVALID), (dict(max_kv=65), INVALID),
+    (dict(npages=0), INVALID), (dict(max_pages=0), INVALID), (dict(page=0), UNSUPPORTED), (dict(page=48), UNSUPPORTED),
+    (dict(page=256), UNSUPPORTED), (dict(npages=1 << 28), UNSUPPORTED), (dict(max_pages=1 << 27), UNSUPPORTED)])
+def test_paged_refusals(kw, status):
+    L = _native.lib()
+    n = ctypes.c_size_t(77)
+    p = ctypes.byref(_paged(**kw))
+    assert L.hsa_paged_workspace_size(p, ctypes.byref(n)) == status
+    assert n.value == 77
+    assert L.hsa_paged_attend(p, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, BIG, None) == status
+    assert L.hsa_paged_append(p, None, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, BIG, None) == status
+
+
+def _each(fn, args, optional=()):
+    """The call with each pointer missing, then misaligned, in turn."""
+    for i, a in enumerate(args):
+        if a != PTR:
+            continue
+        for bad in ((None,) if i not in optional else ()) + (PTR + 2,):
+            yield i, bad, fn(*(bad if j == i else x for j, x in enumerate(args)))
+
+
+def test_pointers_and_workspaces():
+    L = _native.lib()
+    p, g = ctypes.byref(_window()), ctypes.byref(_paged())
+    r = hsa.make_rope(64)
+    for i, bad, got in _each(L.hsa_window_attend, (p, PTR, PTR, PTR, PTR, PTR, None, BIG, None), optional=(5,)):
+        assert got == INVALID, (i, bad)
+    for i, bad, got in _each(L.hsa_window_backward, (p,) + (PTR,) * 9 + (None, BIG, None)):
+        assert got == INVALID, (i, bad)
+    for i, bad, got in _each(L.hsa_paged_attend, (g,) + (PTR,) * 7 + (None, BIG, None)):
+        assert got == INVALID, (i, bad)
+    args = (g, ctypes.byref(r), PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, None, BIG, None)
+    for i, bad, got in _each(L.hsa_paged_append, args, optional=(4,)):
+        assert got == INVALID, (i, bad)
+    for i, bad, got in _each(L.hsa_rope, (ctypes.byref(r), p, PTR, 0, PTR, PTR, PTR, PTR, None), optional=(2, 4, 5)):
+        assert got == INVALID, (i, bad)
+    assert L.hsa_rope(ctypes.byref(r), p, None, 0, None, None, PTR, PTR, None) == INVALID
+    n = ctypes.c_size_t()
+    small = ctypes.byref(_window(B=1, Tq=1, Tkv=90000, q_pos0=89999, window=0))
+    for call, prob, size in ((L.hsa_window_attend, small, L.hsa_window_workspace_size),
+                             (L.hsa_window_backward, p, L.hsa_window_backward_workspace_size)):
+        assert size(prob, ctypes.byref(n)) == 0 and n.value >= 256
+        k = 5 if call is L.hsa_window_attend else 9
+        assert call(prob, *(PTR,) * k, PTR, n.value - 1, None) == WORKSPACE
+        assert call(prob, *(PTR,) * k, None, n.value, None) == WORKSPACE
+        assert call(prob, *(PTR,) * k, PTR + 16, n.value, None) == WORKSPACE
+    assert L.hsa_paged_append(g, None, *(PTR,) * 9, PTR, 255, None) == WORKSPACE
+    for f in (L.hsa_window_workspace_size, L.hsa_window_backward_workspace_size):
+        assert f(None, ctypes.byref(n)) == INVALID and f(p, None) == INVALID
+    assert L.hsa_paged_workspace_size(None, ctypes.byref(n)) == INVALID
+    assert L.hsa_paged_workspace_size(g, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="linear", factor=4.0), dict(scaling="ntk", factor=8.0),
+                                dict(scaling="yarn", factor=16.0, orig_len=4096),
+                                dict(scaling="bands", factor=8.0, orig_len=8192, theta=5e5),
+                                dict(scaling="yarn", factor=4.0, orig_len=2048, low=2.0, high=20.0)])
+@pytest.mark.parametrize("rot", [4, 20, 64, 128])
+def test_rope_frequencies(rot, kw):
+    r = hsa.make_rope(rot, **kw)
+    f, m = inv_freq(rot, **kw)
+    got = torch.tensor(list(r.inv_freq), dtype=torch.float64)
+    # a handful of 64-bit operations on each side
+    assert float(((got[:rot // 2] - f) / f).abs().max()) < 64 * 2.0 ** -53
+    assert not bool(got[rot // 2:].any())
+    assert abs(r.mult - m) < 1e-14
+    assert hsa.make_rope(rot, mscale=0.7, **kw).mult == 0.7
+
+
+@pytest.mark.parametrize("kw", [dict(rot=0), dict(rot=3), dict(rot=130), dict(theta=1.0), dict(theta=math.nan),
+                                dict(theta=math.inf), dict(factor=0.5), dict(factor=math.nan), dict(factor=math.inf),
+                                dict(scaling="yarn"), dict(scaling="bands"), dict(scaling="ntk", rot=2, factor=2.0),
+                                dict(scaling="yarn", orig_len=64, low=3.0, high=3.0), dict(mscale=-1.0),
+                                dict(scaling="bands", orig_len=64, low=-1.0, high=3.0), dict(mscale=math.inf)])
+def test_rope_refusals(kw):
+    with pytest.raises(hsa.HSAError) as e:
+        hsa.make_rope(**{**dict(rot=64), **kw})
+    assert e.value.status == INVALID
+
+
+def test_rope_call_refusals():
+    L = _native.lib()
+    p = ctypes.byref(_window(d=64, H=4, Hkv=2))
+    assert L.hsa_rope_init(None) == INVALID
+    for r in (hsa.make_rope(128), hsa_rope_t()):       # wider than the head; never set up
+        assert L.hsa_rope(ctypes.byref(r), p, None, 0, PTR, PTR, PTR, PTR, None) == INVALID
+    r = ctypes.byref(hsa.make_rope(64))
+    assert L.hsa_rope(None, p, None, 0, PTR, PTR, PTR, PTR, None) == INVALID
+    assert L.hsa_rope(r, None, None, 0, PTR, PTR, PTR, PTR, None) == INVALID
+    bad = hsa_rope_t(64, 0, 9, 0, 1e4, 1.0)
+    assert L.hsa_rope_init(ctypes.byref(bad)) == INVALID
+    bad = hsa_rope_t(64, 2, 0, 0, 1e4, 1.0)
+    assert L.hsa_rope_init(ctypes.byref(bad)) == INVALID
+    with pytest.raises(ValueError):
+        hsa.make_rope(64, scaling="other")
+
+
+def test_binding_refusals():
+    x = torch.zeros(1, 4, 2, 64)
+    for call in (lambda: hsa.window_attend(x, x, x, 3), lambda: hsa.rope(hsa.make_rope(64), x),
+                 lambda: hsa.window_backward(x, x, x, x, x, x, 3), lambda: hsa.rope(hsa.make_rope(64))):
+        with pytest.raises(ValueError):
+            call()
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        hsa.paged_attend(x[0], x, x, i, i[:1], i[None])
+    with pytest.raises(ValueError):
+        hsa.paged_append(x[0], x[0], x, x, i, i[:1], i[None])
+
+
+def test_nothing_to_do_needs_no_pointers():
+    L = _native.lib()
+    ws = (ctypes.c_char * 1024)()
+    at = (ctypes.addressof(ws) + 255) & ~255
+    for kw in (dict(B=0), dict(Tq=0)):
+        p = ctypes.byref(_window(**kw))
+        assert L.hsa_window_attend(p, None, None, None, None, None, at, 512, None) == 0
+        assert L.hsa_rope(ctypes.byref(hsa.make_rope(64)), p, None, 0, None, None, None, None, None) == 0
+    g = ctypes.byref(_paged(rows=0))
+    assert L.hsa_paged_attend(g, *(None,) * 7, at, 512, None) == 0
+    assert L.hsa_paged_append(g, None, *(None,) * 9, at, 512, None) == 0
