@@ -140,6 +140,8 @@ BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt);
 
 cudaError_t launch_simt(const LocArgs &a, int dtype, const void *Q, const void *K, const void *V, void *O,
                         cudaStream_t st);
+bool tc_supported(const LocArgs &a, int dtype);
+cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st);
 cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st);
 cudaError_t launch_bwd_simt(const BwdArgs &w, int dtype, const void *Q, const void *K, const void *V, const void *dO,

@@ -133,7 +133,7 @@ hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, c
     a.nsplit = pl.nsplit;
     a.opart = (float *)((char *)ws + pl.opart);
     a.lpart = (float *)((char *)ws + pl.lpart);
-    cudaError_t e = launch_simt(a, dtype, Q, K, V, O, st);
+    cudaError_t e = pl.tc ? launch_tc(a, Q, K, V, O, st) : launch_simt(a, dtype, Q, K, V, O, st);
     if (e == cudaSuccess && a.nsplit > 1) e = launch_combine(a, dtype, O, st);
     return e == cudaSuccess ? HSA_OK : cuda_fail(e, "local attention kernel launch");
 }
@@ -141,16 +141,16 @@ hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, c
 }  // namespace
 
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
-    (void)dtype;
-    (void)simt;
     LocPlan p{};
-    const int tok = 64 / a.G, bk = 64;
+    p.tc = !simt && tc_supported(a, dtype);
+    const int tok = p.tc ? 2 * (128 / a.G) : 64 / a.G, bk = p.tc ? 128 : 64;
     const long long items = (long long)ceil_div(a.max_q, tok) * a.Hkv * a.B;
-    // too few blocks to fill the SMs twice: the key axis is split over CTAs as well, two tiles each at least
-    const int nt = ceil_div(most_keys(a, tok), bk) + 1;
+    // too few blocks to fill the SMs (CUDA cores: twice): the key axis is split over CTAs as well, two tiles each
+    // at least
+    const int nt = ceil_div(most_keys(a, tok), bk) + 1, want = p.tc ? SMS : 2 * SMS;
     p.nsplit = 1;
-    if (items > 0 && items < 2 * SMS) {
-        int n = ceil_div(2 * SMS, items);
+    if (items > 0 && items < want) {
+        int n = want / (int)items;
         if (n > nt / 2) n = nt / 2;
         if (n > 64) n = 64;
         if (n > 1) p.nsplit = n;
