@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t tmem = bar->tmem_base;   // S/P tiles at 0 and 128, O tiles at 256 and 256 + D
 
     if (warp < 8) {
-        reg_inc<208>();
+        reg_inc<216>();
         // ---------------------------------------------------------------- softmax: thread = row of tile t
         const int t = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(NT, 1)
             const int p = live ? pa + rt : -1;
             // visible keys of this row: [wa, we], and those below sk (<= we as well)
             const int we = min(p, it.s.kv - 1), wa = p >= a.window ? p - a.window + 1 : 0, sk = a.sinks;
-            float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+            float m = -INFINITY;
+            uint64_t l2 = 0;   // row sum, two halves
             for (int i = it.i0; i < it.i1; ++i, ++n) {
                 const int u0 = it.tl.tile(i) * BK;
                 if (!(ok = mbar_wait(&bar->s_full[t], n & 1, abort, status))) break;
@@ -175,38 +176,37 @@ __global__ void __launch_bounds__(NT, 1)
                 if (grow) {
                     f = ex2(m - top);   // 0 from -inf
                     m = top;
-                    l0 *= f;
-                    l1 *= f;
+                    l2 = fma2(l2, pair(f, f), 0);
                 }
                 if (i > it.i0 && __any_sync(FULL, grow)) {
                     // O holds the sums so far: wait for the last product, rescale the rows that need it
                     if (!(ok = mbar_wait(&bar->o_full[t], (n - 1) & 1, abort, status))) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(sO + q * 32, o);
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(sO + q * 16, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                        tmem_st32(sO + q * 32, o);
+                        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                        tmem_st16(sO + q * 16, o);
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
+                const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), mr2 = pair(-ref, -ref);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        float x = __uint_as_float(sr[2 * h + c / 32][c % 32]);
-                        float y = __uint_as_float(sr[2 * h + c / 32][c % 32 + 1]);
-                        fma2(x, y, a.scale_log2, -ref);
+                    for (int c = 0; c < 32; c += 2) {
+                        float x, y;
+                        unpair(fma2(pair(__uint_as_float(sr[q][c]), __uint_as_float(sr[q][c + 1])), sc2, mr2), x, y);
                         x = ex2(x);
                         y = ex2(y);
-                        add2(l0, l1, x, y);
+                        l2 = add2(l2, pair(x, y));
                         pk[c / 2] = pack_bf16x2(x, y);   // the tensor cores take P as bf16
                     }
-                    tmem_st32(sS + h * 32, pk);
+                    tmem_st16(sS + q * 16, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(NT, 1)
             }
             if (!ok) break;
             // epilogue: O / l, or the split's partial and its lse
-            const float l = l0 + l1;
+            float la, lb;
+            unpair(l2, la, lb);
+            const float l = la + lb;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const bool any = it.i1 > it.i0;
             if (any) {
@@ -224,29 +226,31 @@ __global__ void __launch_bounds__(NT, 1)
             }
             const long long row = live ? (long long)(it.s.row0 + tt + rt) * a.H + it.j * a.G + rg : 0;
             const long long prow = (long long)it.split * a.rows * a.H + row;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 if (any) {
                     tmem_ld32(sO + q * 32, o);
                     tmem_wait_ld();
                 }
-                float v[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = l > 0.f ? __uint_as_float(o[c]) * inv : 0.f;
+                for (int c = 0; c < 32; ++c) o[c] = l > 0.f ? __float_as_uint(__uint_as_float(o[c]) * inv) : 0u;
                 if (live) {
                     if (a.nsplit > 1) {
-                        float *dst = a.opart + prow * D + q * 32;
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.opart + prow * D + q * 32);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            *reinterpret_cast<float4 *>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                        for (int c = 0; c < 8; ++c)
+                            dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                     } else {
-                        __nv_bfloat16 *dst = O + row * D + q * 32;
+                        uint4 *dst = reinterpret_cast<uint4 *>(O + row * D + q * 32);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8)
-                            *reinterpret_cast<uint4 *>(dst + c) =
-                                make_uint4(pack_bf16x2(v[c], v[c + 1]), pack_bf16x2(v[c + 2], v[c + 3]),
-                                           pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                h[x] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * x]), __uint_as_float(o[8 * c + 2 * x + 1]));
+                            dst[c] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
             }
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(NT, 1)
             }
         }
     } else {
-        reg_dec<80>();
+        reg_dec<64>();
         if (warp == 8) {
             // ------------------------------------------------------------ loader
             const int psize = a.paged ? 1 << a.page_shift : BK;
