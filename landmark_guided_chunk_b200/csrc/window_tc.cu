@@ -183,10 +183,13 @@ __global__ void __launch_bounds__(NT, 1)
                 const bool full = __all_sync(FULL, u0 + 127 <= end && (u0 >= wa || u0 + 127 < a.sinks));
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 tmem_ld32(sS, sr[0]);
+                tmem_ld32(sS + 32, sr[1]);
                 tmem_wait_ld(sr[0]);
+                tmem_wait_ld(sr[1]);
+                tmem_ld32(sS + 64, sr[2]);   // land while the first half is looked at
+                tmem_ld32(sS + 96, sr[3]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if (q < 3) tmem_ld32(sS + q * 32 + 32, sr[q + 1]);   // lands while this quarter is looked at
                     if (!full) {
                         // bits of columns 32 q ..: c <= end and (c >= wa or c < sinks)
                         auto below = [&](int x) -> uint32_t {   // columns below key x
@@ -201,28 +204,30 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int c = 0; c < 32; c += 2)
                         mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(sr[q][c]), __uint_as_float(sr[q][c + 1]));
-                    if (q < 3) tmem_wait_ld(sr[q + 1]);
+                    if (q == 1) {
+                        tmem_wait_ld(sr[2]);
+                        tmem_wait_ld(sr[3]);
+                    }
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                const bool grow = top > m + RESCALE || (m == -INFINITY && top > m);
-                float f = 1.f;
-                if (grow) {
-                    f = ex2(m - top);   // 0 from -inf
-                    m = top;
+                const bool grow = top > m + RESCALE;   // from m = -inf: with the first visible key
+                if (__any_sync(FULL, grow)) {
+                    const float f = grow ? ex2(m - top) : 1.f;   // 0 from -inf
+                    m = grow ? top : m;
                     l2 = fma2(l2, pair(f, f), 0);
-                }
-                if (i > i0 && __any_sync(FULL, grow)) {
-                    // O holds the sums so far: wait for the last product, rescale the rows that need it
-                    if (!(ok = mbar_wait(&bar->o_full[t], (n - 1) & 1, abort, status))) break;
-                    tc_fence_after();
+                    if (i > i0) {
+                        // O holds the sums so far: wait for the last product, rescale the rows that need it
+                        if (!(ok = mbar_wait(&bar->o_full[t], (n - 1) & 1, abort, status))) break;
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t o[16];
-                        tmem_ld16(sO + q * 16, o);
-                        tmem_wait_ld(o);
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(sO + q * 16, o);
+                            tmem_wait_ld(o);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                        tmem_st16(sO + q * 16, o);
+                            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            tmem_st16(sO + q * 16, o);
+                        }
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
@@ -410,10 +415,11 @@ __global__ void __launch_bounds__(NT, 1)
                     kvpar ^= 1u << st;
                     return r;
                 };
-                auto qk = [&](int t, uint32_t st, int width) {
+                auto qk = [&](int t, uint32_t st, int width, auto &&wait) -> bool {
                     const uint64_t qd = desc_kmajor_sw128(q0 + uniform(x * 2 + t) * C::TILE);
                     const uint64_t kd = desc_kmajor_sw128(kv0 + uniform(st) * C::TILE);
                     const uint32_t id = uniform(idesc_bf16_f32(MR, width, 0, 0)), dst = uniform(t) * 128;
+                    if (!wait()) return false;   // the operands' addresses are ready before the operands
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -426,10 +432,12 @@ __global__ void __launch_bounds__(NT, 1)
                         if (t == it.ntile - 1) umma_commit(&bar->kv_empty[st]);
                     }
                     __syncwarp();
+                    return true;
                 };
-                auto pv = [&](int t, int h, uint32_t st, int w16, bool first) {
+                auto pv = [&](int t, int h, uint32_t st, int w16, bool first, auto &&wait) -> bool {
                     const uint64_t vd = desc_mnmajor_sw128(kv0 + uniform(st) * C::TILE, 16384, 1024);
                     const uint32_t ut = uniform(t), acc = uniform(first ? 0 : 1);
+                    if (!wait()) return false;
                     tc_fence_after();
                     if (elect_one()) {
                         // 16 keys a step: 2048 bytes down V, 8 columns along P
@@ -451,31 +459,30 @@ __global__ void __launch_bounds__(NT, 1)
                         }
                     }
                     __syncwarp();
+                    return true;
                 };
                 // first scores of both tiles
                 uint32_t ks = head;
                 ok = wait_kv(ks);
                 for (int t = 0; t < it.ntile && ok; ++t) {
-                    if (!(ok = mbar_wait(&bar->q_full[x][t], qpar >> (2 * x + t) & 1, abort, status))) break;
+                    ok = qk(t, ks, it.tl.width(it.i0), [&] {
+                        return mbar_wait(&bar->q_full[x][t], qpar >> (2 * x + t) & 1, abort, status);
+                    });
                     qpar ^= 1u << (2 * x + t);
-                    qk(t, ks, it.tl.width(it.i0));
                 }
                 for (int i = 0; i < nt && ok; ++i) {
                     const uint32_t vs = after(ks), kn = after(vs);
                     const int w16 = it.tl.width(it.i0 + i) >> 4;
                     for (int t = 0; t < it.ntile && ok; ++t) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {   // P comes in halves
-                            if (!(ok = mbar_wait(&bar->p_full[t][h], p_par >> t & 1, abort, status))) break;
-                            if (t == 0 && h == 0 && !(ok = wait_kv(vs))) break;
-                            pv(t, h, vs, w16, i == 0);
-                        }
-                        if (!ok) break;
+                        // P comes in halves
+                        ok = pv(t, 0, vs, w16, i == 0, [&] {
+                            return (t > 0 || wait_kv(vs)) && mbar_wait(&bar->p_full[t][0], p_par >> t & 1, abort, status);
+                        });
+                        ok = ok && pv(t, 1, vs, w16, i == 0, [&] {
+                            return mbar_wait(&bar->p_full[t][1], p_par >> t & 1, abort, status);
+                        });
                         p_par ^= 1u << t;
-                        if (i + 1 < nt) {
-                            if (t == 0 && !(ok = wait_kv(kn))) break;
-                            qk(t, kn, it.tl.width(it.i0 + i + 1));
-                        }
+                        if (i + 1 < nt) ok = ok && qk(t, kn, it.tl.width(it.i0 + i + 1), [&] { return t > 0 || wait_kv(kn); });
                     }
                     ks = kn;
                     head = after(vs);
