@@ -140,6 +140,9 @@ BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt);
 
 cudaError_t launch_simt(const LocArgs &a, int dtype, const void *Q, const void *K, const void *V, void *O,
                         cudaStream_t st);
+constexpr int FEW_CLUSTER = 8;   // splits that the few-row kernel joins within a cluster
+bool few_supported(const LocArgs &a, int dtype);
+cudaError_t launch_few(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 bool tc_supported(const LocArgs &a, int dtype);
 cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st);

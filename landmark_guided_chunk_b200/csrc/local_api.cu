@@ -133,8 +133,10 @@ hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, c
     a.nsplit = pl.nsplit;
     a.opart = (float *)((char *)ws + pl.opart);
     a.lpart = (float *)((char *)ws + pl.lpart);
-    cudaError_t e = pl.tc ? launch_tc(a, Q, K, V, O, st) : launch_simt(a, dtype, Q, K, V, O, st);
-    if (e == cudaSuccess && a.nsplit > 1) e = launch_combine(a, dtype, O, st);
+    cudaError_t e = pl.few ? launch_few(a, Q, K, V, O, st)
+                    : pl.tc ? launch_tc(a, Q, K, V, O, st)
+                            : launch_simt(a, dtype, Q, K, V, O, st);
+    if (e == cudaSuccess && a.nsplit > (pl.few ? FEW_CLUSTER : 1)) e = launch_combine(a, dtype, O, st);
     return e == cudaSuccess ? HSA_OK : cuda_fail(e, "local attention kernel launch");
 }
 
@@ -142,22 +144,35 @@ hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, c
 
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
     LocPlan p{};
-    p.tc = !simt && tc_supported(a, dtype);
-    const int tok = p.tc ? 2 * (128 / a.G) : 64 / a.G, bk = p.tc ? 128 : 64;
-    const long long items = (long long)ceil_div(a.max_q, tok) * a.Hkv * a.B;
-    // too few blocks to fill the SMs (CUDA cores: twice): the key axis is split over CTAs as well, two tiles each
-    // at least
-    const int nt = ceil_div(most_keys(a, tok), bk) + 1, want = p.tc ? SMS : 2 * SMS;
     p.nsplit = 1;
-    if (items > 0 && items < want) {
-        int n = want / (int)items;
-        if (n > nt / 2) n = nt / 2;
+    p.few = !simt && few_supported(a, dtype);
+    p.tc = !p.few && !simt && tc_supported(a, dtype);
+    if (p.few) {
+        // CTAs of 64-key tiles, two per SM.  A cluster joins up to 8 splits in the same launch; more splits
+        // (partials and a second launch, ~3 us) only where 8 leave most SMs without work for long.
+        const long long items = (long long)a.Hkv * a.B;
+        const int nt = ceil_div(most_keys(a, a.max_q), 64) + 1;
+        long long n = items > 0 ? 2 * SMS / items : 1;
+        if (n > FEW_CLUSTER && (nt < 32 * FEW_CLUSTER || items * FEW_CLUSTER >= SMS)) n = FEW_CLUSTER;
+        if (n > nt) n = nt;
         if (n > 64) n = 64;
-        if (n > 1) p.nsplit = n;
+        if (n > 1) p.nsplit = (int)n;
+    } else {
+        const int tok = p.tc ? 2 * (128 / a.G) : 64 / a.G, bk = p.tc ? 128 : 64;
+        const long long items = (long long)ceil_div(a.max_q, tok) * a.Hkv * a.B;
+        // too few blocks to fill the SMs (CUDA cores: twice): the key axis is split over CTAs as well, two tiles
+        // each at least
+        const int nt = ceil_div(most_keys(a, tok), bk) + 1, want = p.tc ? SMS : 2 * SMS;
+        if (items > 0 && items < want) {
+            int n = want / (int)items;
+            if (n > nt / 2) n = nt / 2;
+            if (n > 64) n = 64;
+            if (n > 1) p.nsplit = n;
+        }
     }
     size_t off = HDR;
     p.opart = p.lpart = off;
-    if (p.nsplit > 1) {
+    if (p.nsplit > (p.few ? FEW_CLUSTER : 1)) {
         const size_t r = (size_t)a.rows * a.H * p.nsplit;
         off += align256(r * a.d * sizeof(float));
         p.lpart = off;
