@@ -149,6 +149,9 @@ cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st
 cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st);
 cudaError_t launch_bwd_simt(const BwdArgs &w, int dtype, const void *Q, const void *K, const void *V, const void *dO,
                             void *dQ, void *dK, void *dV, cudaStream_t st);
+bool bwd_tc_supported(const LocArgs &a, int dtype);
+cudaError_t launch_bwd_tc(const BwdArgs &w, const void *Q, const void *K, const void *V, const void *dO, void *dQ,
+                          void *dK, void *dV, cudaStream_t st);
 cudaError_t launch_bwd_join(const BwdArgs &w, int bk, int dtype, void *dK, void *dV, cudaStream_t st);
 
 struct RopeArgs {

@@ -183,10 +183,9 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
 }
 
 BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt) {
-    (void)dtype;
-    (void)simt;
     BwdPlan p{};
-    p.bk = 64;
+    p.tc = !simt && bwd_tc_supported(a, dtype);
+    p.bk = p.tc ? 128 : 64;
     p.nkt = ceil_div(a.max_kv, p.bk);
     const int sinks = a.sinks < a.max_kv ? a.sinks : a.max_kv;
     if (a.window < INT32_MAX && sinks > 0 && a.max_q > 0 && (long long)a.q_pos0 + a.max_q - 1 >= a.window) {
@@ -288,7 +287,9 @@ hsa_status_t hsa_window_backward(const hsa_window_t *prob, const void *Q, const 
     }
     if (e == cudaSuccess && rows) {
         e = launch_rowdot(a, prob->dtype, O, dO, w.D, st);
-        if (e == cudaSuccess) e = launch_bwd_simt(w, prob->dtype, Q, K, V, dO, dQ, dK, dV, st);
+        if (e == cudaSuccess)
+            e = pl.tc ? launch_bwd_tc(w, Q, K, V, dO, dQ, dK, dV, st)
+                      : launch_bwd_simt(w, prob->dtype, Q, K, V, dO, dQ, dK, dV, st);
         if (e == cudaSuccess) e = launch_bwd_join(w, pl.bk, prob->dtype, dK, dV, st);
     }
     return e == cudaSuccess ? HSA_OK : cuda_fail(e, "local attention backward launch");
