@@ -30,6 +30,36 @@ __device__ __forceinline__ bool elect_one() {
 // x (the same on every lane) as a value that the compiler knows to be uniform
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(FULL, x); }
 
+// Whether the phase with `parity` has completed, without waiting; the same answer on every lane.
+__device__ __forceinline__ bool mbar_test_warp(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P1;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P1;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(FULL, ok != 0);
+}
+
+// Bound for a loop that polls several barriers: call once per round without progress.
+struct PollLimit {
+    uint32_t n = 0;
+    uint64_t t0 = 0;
+    __device__ __forceinline__ void progress() { n = 0, t0 = 0; }
+    __device__ __forceinline__ bool expired(volatile int *abort, uint32_t *status) {
+        if ((++n & 255u) != 0) return false;
+        if (__any_sync(FULL, *abort)) return true;
+        const uint64_t t = __shfl_sync(FULL, globaltimer_ns(), 0);
+        if (t0 == 0) t0 = t;
+        if (t - t0 <= WAIT_LIMIT_NS) return false;
+        *abort = 1;
+        atomicOr(status, DEV_TIMEOUT);
+        return true;
+    }
+};
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(

@@ -250,19 +250,35 @@ __global__ void __launch_bounds__(256) combine_kernel(LocArgs a, T *__restrict__
     if (lane == 0 && a.lse) a.lse[row] = l > 0.f ? mx + logf(l) : -INFINITY;
 }
 
-// D[row] = sum_x dO[row][x] O[row][x], one warp per row.
+// D[row] = sum_x dO[row][x] O[row][x]: 16-byte loads, the lanes of a row side by side, four rows in flight per lane.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) rowdot_kernel(const T *__restrict__ O, const T *__restrict__ dO,
                                                      float *__restrict__ out, long long n) {
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    constexpr int V = 16 / sizeof(T), LPR = D / V, RPW = 32 / LPR, U = 4;   // lanes per row, rows per warp and load
     const int lane = threadIdx.x & 31;
-    if (row >= n) return;
-    constexpr int N = D / 32;
-    float s = 0.f;
+    const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * RPW * U + lane / LPR;
+    uint4 o[U], g[U];
 #pragma unroll
-    for (int x = 0; x < N; ++x) s = fmaf(to_f32(O[row * D + lane * N + x]), to_f32(dO[row * D + lane * N + x]), s);
-    s = warp_sum(s);
-    if (lane == 0) out[row] = s;
+    for (int u = 0; u < U; ++u) {
+        const long long r = r0 + u * RPW;
+        if (r < n) {
+            o[u] = reinterpret_cast<const uint4 *>(O + r * D)[lane % LPR];
+            g[u] = reinterpret_cast<const uint4 *>(dO + r * D)[lane % LPR];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long long r = r0 + u * RPW;
+        float s = 0.f;
+        if (r < n) {
+            const T *x = reinterpret_cast<const T *>(&o[u]), *y = reinterpret_cast<const T *>(&g[u]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s = fmaf(to_f32(x[e]), to_f32(y[e]), s);
+        }
+#pragma unroll
+        for (int w = LPR / 2; w > 0; w >>= 1) s += __shfl_xor_sync(FULL, s, w);
+        if (r < n && lane % LPR == 0) out[r] = s;
+    }
 }
 
 // dQ: the forward's iteration; P from lse, dP = dO V^T, dS = P (dP - D), dQ += dS K.
@@ -522,7 +538,8 @@ cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st
 cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st) {
     const long long n = (long long)a.rows * a.H;
     if (n == 0) return cudaSuccess;
-    const unsigned g = (unsigned)((n + 7) / 8);
+    const int per = 8 * 4 * 32 / (a.d / (dtype == HSA_F32 ? 4 : 8));   // rows per block
+    const unsigned g = (unsigned)((n + per - 1) / per);
     if (dtype == HSA_F32) {
         if (a.d == 64) rowdot_kernel<float, 64><<<g, 256, 0, st>>>((const float *)O, (const float *)dO, D, n);
         else rowdot_kernel<float, 128><<<g, 256, 0, st>>>((const float *)O, (const float *)dO, D, n);
