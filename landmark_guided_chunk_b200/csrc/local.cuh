@@ -24,7 +24,8 @@ struct LocArgs {
     int paged, page_shift, npages, max_pages;
     const int32_t *q_start, *kv_len, *table;
     int nsplit;            // key-axis splits per (sequence, kv head, row tile)
-    float *opart, *lpart;  // split partials: [nsplit][rows][H][d] and [nsplit][rows][H]
+    float *opart, *lpart;  // split partials: [nsplit][rows][H][d] and [nsplit][rows][H] (tcgen05: by slot)
+    long long *tc_starts;  // tcgen05: starts of the blocks' key tiles when CTAs take equal shares of them; else null
     float *lse;            // optional output
     uint32_t *status;
 };
@@ -51,7 +52,7 @@ __device__ __forceinline__ Seq seq_of(const LocArgs &a, int b) {
     s.n = min(r1c - s.row0, a.max_q);
     s.kv = min(max(kv, 0), a.max_kv);
     s.pos0 = s.kv - s.n;
-    if (threadIdx.x == 0 && (s.row0 != r0 || s.row0 + s.n != r1 || s.kv != kv)) atomicOr(a.status, DEV_BAD_INDEX);
+    if (s.row0 != r0 || s.row0 + s.n != r1 || s.kv != kv) atomicOr(a.status, DEV_BAD_INDEX);
     return s;
 }
 
@@ -124,10 +125,12 @@ struct BwdArgs {
     float *part;                     // [2 (dK, dV)][nfar + 1][B][Hkv][nst * BK][d]
 };
 
+long long most_keys(const LocArgs &a, int tok);   // that `tok` consecutive queries can see, at most
+
 struct LocPlan {
     bool tc, few;          // forward path: tcgen05 tiles, few-row kernel; neither: CUDA-core tiles
     int nsplit;
-    size_t opart, lpart, total;
+    size_t opart, lpart, starts, total;   // offsets; starts 0: no shares
 };
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt);
 
@@ -144,6 +147,11 @@ constexpr int FEW_CLUSTER = 8;   // splits that the few-row kernel joins within 
 bool few_supported(const LocArgs &a, int dtype);
 cudaError_t launch_few(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 bool tc_supported(const LocArgs &a, int dtype);
+struct TcPlan {
+    bool shares;                    // CTAs take equal shares of all key tiles; else whole items
+    size_t starts, opart, lpart;    // bytes
+};
+TcPlan tc_plan(const LocArgs &a, long long most_keys);   // most_keys: that one block can see
 cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st);
 cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st);

@@ -117,13 +117,6 @@ hsa_status_t need4(const void *x, const char *name) {
     return HSA_OK;
 }
 
-// Keys that one block of `tok` query tokens can see, at most.
-long long most_keys(const LocArgs &a, int tok) {
-    if (a.window == INT32_MAX) return a.max_kv;
-    const long long w = (long long)a.window + tok - 1 + a.sinks;
-    return w < a.max_kv ? w : a.max_kv;
-}
-
 hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, const void *K, const void *V, void *O,
                          void *ws, size_t ws_bytes, cudaStream_t st) {
     const LocPlan pl = plan_forward(a, dtype, (flags & HSA_FLAG_SIMT) != 0);
@@ -133,6 +126,7 @@ hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, c
     a.nsplit = pl.nsplit;
     a.opart = (float *)((char *)ws + pl.opart);
     a.lpart = (float *)((char *)ws + pl.lpart);
+    a.tc_starts = pl.starts ? (long long *)((char *)ws + pl.starts) : nullptr;
     cudaError_t e = pl.few ? launch_few(a, Q, K, V, O, st)
                     : pl.tc ? launch_tc(a, Q, K, V, O, st)
                             : launch_simt(a, dtype, Q, K, V, O, st);
@@ -141,6 +135,12 @@ hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, c
 }
 
 }  // namespace
+
+long long most_keys(const LocArgs &a, int tok) {
+    if (a.window == INT32_MAX) return a.max_kv;
+    const long long w = (long long)a.window + tok - 1 + a.sinks;
+    return w < a.max_kv ? w : a.max_kv;
+}
 
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
     LocPlan p{};
@@ -157,14 +157,13 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
         if (n > nt) n = nt;
         if (n > 64) n = 64;
         if (n > 1) p.nsplit = (int)n;
-    } else {
-        const int tok = p.tc ? 2 * (128 / a.G) : 64 / a.G, bk = p.tc ? 128 : 64;
+    } else if (!p.tc) {
+        const int tok = 64 / a.G, bk = 64;
         const long long items = (long long)ceil_div(a.max_q, tok) * a.Hkv * a.B;
-        // too few blocks to fill the SMs (CUDA cores: twice): the key axis is split over CTAs as well, two tiles
-        // each at least
-        const int nt = ceil_div(most_keys(a, tok), bk) + 1, want = p.tc ? SMS : 2 * SMS;
-        if (items > 0 && items < want) {
-            int n = want / (int)items;
+        // too few blocks to fill the SMs twice: the key axis is split over CTAs as well, two tiles each at least
+        const int nt = ceil_div(most_keys(a, tok), bk) + 1;
+        if (items > 0 && items < 2 * SMS) {
+            int n = 2 * SMS / (int)items;
             if (n > nt / 2) n = nt / 2;
             if (n > 64) n = 64;
             if (n > 1) p.nsplit = n;
@@ -172,7 +171,17 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
     }
     size_t off = HDR;
     p.opart = p.lpart = off;
-    if (p.nsplit > (p.few ? FEW_CLUSTER : 1)) {
+    if (p.tc) {
+        const TcPlan t = tc_plan(a, most_keys(a, 2 * (128 / a.G)));
+        if (t.shares) {
+            p.starts = off;
+            off += align256(t.starts);
+            p.opart = off;
+            off += align256(t.opart);
+            p.lpart = off;
+            off += align256(t.lpart);
+        }
+    } else if (p.nsplit > (p.few ? FEW_CLUSTER : 1)) {
         const size_t r = (size_t)a.rows * a.H * p.nsplit;
         off += align256(r * a.d * sizeof(float));
         p.lpart = off;

@@ -37,11 +37,16 @@ template <int D> struct Cfg {
     static constexpr int NST = D == 128 ? 3 : 8;       // K/V ring stages
 };
 
+struct Share {
+    int g, j, i, left;   // block, kv head, key tile to start with; key tiles to take
+};
+
 struct __align__(8) Bars {
     uint64_t q_full[2][2], q_empty[2][2], kv_full[8], kv_empty[8], land[8];   // q: [buffer][tile]
     uint64_t s_full[2], p_full[2][2], o_full[2], out_full[2], done;           // p: [tile][half of its keys]
     uint32_t tmem_base;
     int abort;
+    Share share;
     int row[2][MR];               // token of each row's output (-1: padding)
 };
 
@@ -79,28 +84,179 @@ __device__ __forceinline__ KeyTiles key_tiles(int pa, int pb, int kv, int window
 }
 
 struct Item {
-    int b, j, split, t0, ntile;   // ntile: row tiles with tokens (0: nothing to do)
-    int i0, i1;                   // key tiles of this split
+    int b, j, t0, ntile;          // ntile: row tiles with tokens (0: nothing to do)
+    int i0, i1;                   // key tiles to do
+    int slot;                     // partials' slot of an item that is shared with other CTAs; -1: all of it is this CTA's
     Seq s;
     KeyTiles tl;
 };
 
-__device__ __forceinline__ Item item_of(const LocArgs &a, int idx, int tok, int nblk) {
+// Block g of two row tiles: (sequence, block of 2 tok tokens); without a window, later blocks see more keys:
+// longest first.
+__device__ __forceinline__ void block_of(const LocArgs &a, int g, int tok, int nblk, Item *it) {
+    const int blk = nblk - 1 - g % nblk;
+    it->b = g / nblk;
+    it->s = seq_of(a, it->b);
+    it->t0 = blk * 2 * tok;
+    const int left = it->s.n - it->t0;
+    it->ntile = left <= 0 ? 0 : left <= tok ? 1 : 2;
+    const int pa = it->s.pos0 + it->t0, pb = it->s.pos0 + min(it->s.n, it->t0 + 2 * tok) - 1;
+    it->tl = key_tiles(pa, pb, it->s.kv, a.window, a.sinks, a.paged ? 1 << a.page_shift : 1);
+    if (it->ntile == 0) it->tl.nt = 0;
+}
+
+// Which items a CTA takes.  Many items: every gridDim.x-th one.  Few: the key tiles of all items in a row, cut into
+// equal shares, one per CTA (lengths differ, and whole items would leave most SMs waiting for the longest); an item
+// that a cut goes through is written as partials and joined by join_kernel.
+struct Walk {
+    Share s;             // shares: what is left; else s.g: the next item
+    bool first;
+    __device__ __forceinline__ bool next(const LocArgs &a, bool shares, int tok, int nblk, int nitems, Item *it) {
+        if (!shares) {
+            if (s.g >= nitems) return false;
+            it->j = s.g % a.Hkv;
+            block_of(a, s.g / a.Hkv, tok, nblk, it);
+            it->i0 = 0;
+            it->i1 = it->tl.nt;
+            it->slot = -1;
+            s.g += gridDim.x;
+            return true;
+        }
+        if (s.left <= 0) return false;
+        int weight;
+        while (true) {
+            block_of(a, s.g, tok, nblk, it);
+            weight = it->ntile == 0 ? 0 : max(it->tl.nt, 1);   // a block that sees no key still writes its zeros
+            if (weight > 0) break;
+            ++s.g;
+        }
+        const int take = min(s.left, weight - s.i);
+        it->j = s.j;
+        it->i0 = s.i;
+        it->i1 = min(s.i + take, it->tl.nt);
+        it->slot = take < weight ? 2 * (int)blockIdx.x + (first ? 0 : 1) : -1;
+        first = false;
+        s.left -= take;
+        s.i += take;
+        if (s.i == weight) {
+            s.i = 0;
+            if (++s.j == a.Hkv) {
+                s.j = 0;
+                ++s.g;
+            }
+        }
+        return true;
+    }
+};
+
+// Start of CTA c's share in the row of `total` tiles that `ctas` CTAs divide.
+__device__ __forceinline__ long long share_start(long long total, int ctas, int c) { return total * c / ctas; }
+constexpr int SHARE_LEAST = 8;   // key tiles per CTA at least: a cut's partials and their join cost about four
+
+// One warp: the sum of all blocks' tiles times kv heads, and this CTA's share of them.  CTA 0 leaves the blocks'
+// starts in `starts` (int64 [blocks + 1], then the number of CTAs) for the join.
+__device__ __forceinline__ Share find_share(const LocArgs &a, int tok, int nblk, long long *starts) {
+    const int lane = threadIdx.x & 31, nb = a.B * nblk;
+    auto weight_of = [&](int g) -> int {
+        if (g >= nb) return 0;
+        Item it;
+        block_of(a, g, tok, nblk, &it);
+        return it.ntile == 0 ? 0 : max(it.tl.nt, 1) * a.Hkv;
+    };
+    long long total = 0;
+    for (int g0 = 0; g0 < nb; g0 += 32) total += __reduce_add_sync(FULL, (unsigned)weight_of(g0 + lane));
+    const int ctas = (int)max(1ll, min((long long)gridDim.x, total / SHARE_LEAST));
+    const int c = blockIdx.x;
+    Share sh{0, 0, 0, 0};
+    const long long s0 = share_start(total, ctas, c), s1 = share_start(total, ctas, c + 1);
+    long long at = 0;
+    for (int g0 = 0; g0 < nb; g0 += 32) {
+        const int wl = weight_of(g0 + lane);
+        int inc = wl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const long long before = at + inc - wl;
+        if (c == 0 && g0 + lane < nb) starts[g0 + lane] = before;
+        if (c < ctas && wl > 0 && before <= s0 && s0 < before + wl) {
+            const int per = wl / a.Hkv, off = (int)(s0 - before);
+            sh.g = g0 + lane;
+            sh.j = off / per;
+            sh.i = off % per;
+            sh.left = (int)(s1 - s0);
+        }
+        at += __shfl_sync(FULL, inc, 31);
+    }
+    if (c == 0 && lane == 0) {
+        starts[nb] = total;
+        starts[nb + 1] = ctas;
+    }
+    sh.g = (int)__reduce_max_sync(FULL, (unsigned)sh.g);   // one lane has found it, the others hold zeros
+    sh.j = (int)__reduce_max_sync(FULL, (unsigned)sh.j);
+    sh.i = (int)__reduce_max_sync(FULL, (unsigned)sh.i);
+    sh.left = (int)__reduce_max_sync(FULL, (unsigned)sh.left);
+    return sh;
+}
+
+// Joins the partials of the items that the shares cut: O = sum exp(lse_i - lse) O_i, in order of the pieces.  One
+// block per (item, row tile).
+template <int D>
+__global__ void __launch_bounds__(256)
+    window_join_kernel(const __grid_constant__ LocArgs a, __nv_bfloat16 *__restrict__ O, int tok, int nblk, const long long *starts) {
+    const int nb = a.B * nblk, g = blockIdx.x / a.Hkv, j = blockIdx.x % a.Hkv, t = blockIdx.y;
+    const long long total = starts[nb], s = starts[g], e = starts[g + 1];
+    const int ctas = (int)starts[nb + 1];
+    if (e == s) return;
+    const long long per = (e - s) / a.Hkv, i0 = s + j * per, i1 = i0 + per;
+    // CTA of a tile: the c with share_start(c) <= tile < share_start(c + 1)
+    auto cta_of = [&](long long x) -> int {
+        int c = (int)(x * ctas / total);
+        while (c + 1 < ctas && share_start(total, ctas, c + 1) <= x) ++c;
+        while (share_start(total, ctas, c) > x) --c;
+        return c;
+    };
+    const int c0 = cta_of(i0), pieces = cta_of(i1 - 1) - c0 + 1;
+    if (pieces == 1) return;
+    // the piece is its CTA's first item unless that CTA started before it
+    __shared__ int slot[148];
+    if (threadIdx.x < pieces)
+        slot[threadIdx.x] = 2 * (c0 + threadIdx.x) + (share_start(total, ctas, c0 + threadIdx.x) >= i0 ? 0 : 1);
+    __syncthreads();
     Item it;
-    it.j = idx % a.Hkv;
-    idx /= a.Hkv;
-    it.split = idx % a.nsplit;
-    idx /= a.nsplit;
-    const int blk = nblk - 1 - idx % nblk;   // without a window, later blocks see more keys: longest first
-    it.b = idx / nblk;
-    it.s = seq_of(a, it.b);
-    it.t0 = blk * 2 * tok;
-    const int left = it.s.n - it.t0;
-    it.ntile = left <= 0 ? 0 : left <= tok ? 1 : 2;
-    const int pa = it.s.pos0 + it.t0, pb = it.s.pos0 + min(it.s.n, it.t0 + 2 * tok) - 1;
-    it.tl = key_tiles(pa, pb, it.s.kv, a.window, a.sinks, a.paged ? 1 << a.page_shift : 1);
-    split_range(it.tl.nt, a.nsplit, it.split, &it.i0, &it.i1);
-    return it;
+    block_of(a, g, tok, nblk, &it);
+    // a thread: four columns of every 256 / (D / 4)-th row
+    constexpr int TPR = D / 4, RPB = 256 / TPR;
+    const int col = threadIdx.x % TPR * 4;
+#pragma unroll 2
+    for (int r = threadIdx.x / TPR; r < tok * a.G; r += RPB) {
+        const int token = it.t0 + t * tok + r / a.G;
+        if (token >= it.s.n) continue;
+        const long long rt = t * MR + r;
+        float mx = -INFINITY;
+        for (int k = 0; k < pieces; ++k) mx = fmaxf(mx, a.lpart[(long long)slot[k] * 2 * MR + rt]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        if (mx != -INFINITY) {
+#pragma unroll 4
+            for (int k = 0; k < pieces; ++k) {
+                const long long at = (long long)slot[k] * 2 * MR + rt;
+                const float w = expf(a.lpart[at] - mx);
+                const float4 v = *reinterpret_cast<const float4 *>(a.opart + at * D + col);
+                l += w;
+                acc.x = fmaf(w, v.x, acc.x);
+                acc.y = fmaf(w, v.y, acc.y);
+                acc.z = fmaf(w, v.z, acc.z);
+                acc.w = fmaf(w, v.w, acc.w);
+            }
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long row = (long long)(it.s.row0 + token) * a.H + j * a.G + r % a.G;
+        *reinterpret_cast<uint2 *>(O + row * D + col) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (col == 0 && a.lse) a.lse[row] = l > 0.f ? mx + logf(l) : -INFINITY;
+    }
 }
 
 template <int D>
@@ -108,7 +264,7 @@ __global__ void __launch_bounds__(NT, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                       __nv_bfloat16 *__restrict__ O,
-                      const __grid_constant__ LocArgs a, int tok, int nblk, int nitems) {
+                      const __grid_constant__ LocArgs a, int tok, int nblk, int nitems, long long *starts) {
     typedef Cfg<D> C;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -145,6 +301,11 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_alloc(&bar->tmem_base, 512);
         tmem_relinquish();
     }
+    const bool shares = starts != nullptr;
+    if (warp == 10) {
+        const Share sh = shares ? find_share(a, tok, nblk, starts) : Share{(int)blockIdx.x, 0, 0, 0};
+        if (lane == 0) bar->share = sh;
+    }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -160,9 +321,13 @@ __global__ void __launch_bounds__(NT, 1)
         const int rt = r / a.G;                  // token in the tile
         uint32_t n = 0, na = 0;                  // tiles of S, items with keys so far
         bool ok = true;
-        for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
-            const Item it = item_of(a, idx, tok, nblk);
-            if (t >= it.ntile) continue;
+        Item it;
+        for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
+            const bool any = it.i1 > it.i0;
+            if (t >= it.ntile) {
+                na += any;
+                continue;
+            }
             const int tt = it.t0 + t * tok;                  // the tile's first token
             const bool live = rt < tok && tt + rt < it.s.n;
             const int p = it.s.pos0 + tt + rt;
@@ -264,17 +429,16 @@ __global__ void __launch_bounds__(NT, 1)
             unpair(l2, la, lb);
             const float l = la + lb;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const bool any = i1 > i0;
             if (any) {
                 if (!(ok = mbar_wait(&bar->o_full[t], (n - 1) & 1, abort, status))) break;
                 tc_fence_after();
             }
             const int token = *(volatile int *)&bar->row[t][r];
             const bool out = token >= 0;
-            const long long row = (long long)token * a.H + idx % a.Hkv * a.G + r % a.G;
-            const long long prow = (long long)(idx / a.Hkv % a.nsplit) * a.rows * a.H + row;
+            const long long row = (long long)token * a.H + it.j * a.G + r % a.G;
+            const long long prow = (long long)it.slot * 2 * MR + t * MR + r;
             // whole tiles go out by TMA from the Q buffer, which no product reads any more
-            const bool whole = a.nsplit == 1 && it.t0 + (t + 1) * tok <= it.s.n;
+            const bool whole = it.slot < 0 && it.t0 + (t + 1) * tok <= it.s.n;
             uint8_t *stage = sQ + ((na & 1) * 2 + t) * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -285,7 +449,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) o[c] = l > 0.f ? __float_as_uint(__uint_as_float(o[c]) * inv) : 0u;
-                if (a.nsplit > 1) {
+                if (it.slot >= 0) {
                     if (out) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.opart + prow * D + q * 32);
 #pragma unroll
@@ -317,7 +481,7 @@ __global__ void __launch_bounds__(NT, 1)
             tc_fence_before();   // these reads come before the next item's product into O (through p_full)
             if (out) {
                 const float lse = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
-                if (a.nsplit > 1)
+                if (it.slot >= 0)
                     a.lpart[prow] = lse;
                 else if (a.lse)
                     a.lse[row] = lse;
@@ -335,8 +499,8 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t qpar = 0;                   // bit 2 x + t: parity of q_full[x][t]'s next phase (and of q_empty's last)
             uint32_t qused = 0;                  // bit 2 x + t: filled before
             bool ok = true;
-            for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
-                const Item it = item_of(a, idx, tok, nblk);
+            Item it;
+            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 for (int i = it.i0; i < it.i1 && ok; ++i) {
                     const int u0 = it.tl.start(i);
@@ -404,8 +568,8 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
             uint32_t qpar = 0, p_par = 0, kvpar = 0, na = 0, head = 0;   // bits: parities of the next phases
             bool ok = true;
-            for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
-                const Item it = item_of(a, idx, tok, nblk);
+            Item it;
+            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 const int nt = it.i1 - it.i0, x = na++ & 1;   // key tiles, Q buffer
                 // ring stages of K and V of tile i and of K of tile i + 1
@@ -495,15 +659,15 @@ __global__ void __launch_bounds__(NT, 1)
             // ------------------------------------------------------------ output tiles, and the release of their buffers
             uint32_t na = 0, par = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
-                const Item it = item_of(a, idx, tok, nblk);
+            Item it;
+            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 const int x = na++ & 1;
                 for (int t = 0; t < it.ntile; ++t) {
                     if (!(ok = mbar_wait(&bar->out_full[t], par >> t & 1, abort, status))) break;
                     par ^= 1u << t;
                     if (lane == 0) {
-                        if (a.nsplit == 1 && it.t0 + (t + 1) * tok <= it.s.n) {
+                        if (it.slot < 0 && it.t0 + (t + 1) * tok <= it.s.n) {
                             for (int y = 0; y < C::NBX; ++y)
                                 tma_store_3d(&tmO, sQ + (x * 2 + t) * C::TILE + y * 16384, 64 * y, it.j * a.G,
                                              it.s.row0 + it.t0 + t * tok);
@@ -519,8 +683,8 @@ __global__ void __launch_bounds__(NT, 1)
             // ------------------------------------------------------------ zeroes dead V rows at the range's edges
             uint32_t nkv = 0, land_par = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
-                const Item it = item_of(a, idx, tok, nblk);
+            Item it;
+            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 for (int i = it.i0; i < it.i1 && ok; ++i, nkv += 2) {
                     if (!it.tl.has_dead(i)) continue;
@@ -557,7 +721,8 @@ bool tc_supported(const LocArgs &a, int dtype) {
 
 cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
     const int tok = MR / a.G, nblk = (a.max_q + 2 * tok - 1) / (2 * tok);
-    const long long items = (long long)a.B * nblk * a.Hkv * a.nsplit;
+    const long long items = (long long)a.B * nblk * a.Hkv;
+    long long *starts = a.tc_starts;
     CUtensorMap mq, mk, mv, mo;
     const uint64_t d = a.d;
     const uint64_t qd[3] = {d, (uint64_t)a.H, (uint64_t)a.rows}, qs[2] = {d * 2, (uint64_t)a.H * d * 2};
@@ -570,16 +735,41 @@ cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void
     if (e == cudaSuccess) e = make_tmap_3d(&mk, K, kd, ks, kb);
     if (e == cudaSuccess) e = make_tmap_3d(&mv, V, kd, ks, kb);
     if (e != cudaSuccess) return e;
-    const int grid = items < 148 ? (int)items : 148;
+    // shares: every SM may get one, however few the items
+    const int grid = items < 148 && !starts ? (int)items : 148;
     auto go = [&](auto kern, int tile, int nst) {
         const size_t smem = 1024 + (size_t)(4 + nst) * tile + sizeof(Bars);
         cudaError_t x = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (x != cudaSuccess) return x;
-        kern<<<grid, NT, smem, st>>>(mq, mk, mv, mo, (__nv_bfloat16 *)O, a, tok, nblk, (int)items);
+        kern<<<grid, NT, smem, st>>>(mq, mk, mv, mo, (__nv_bfloat16 *)O, a, tok, nblk, (int)items, starts);
         return cudaGetLastError();
     };
-    return a.d == 64 ? go(window_fwd_kernel<64>, Cfg<64>::TILE, Cfg<64>::NST)
-                     : go(window_fwd_kernel<128>, Cfg<128>::TILE, Cfg<128>::NST);
+    e = a.d == 64 ? go(window_fwd_kernel<64>, Cfg<64>::TILE, Cfg<64>::NST)
+                  : go(window_fwd_kernel<128>, Cfg<128>::TILE, Cfg<128>::NST);
+    if (e != cudaSuccess || !starts) return e;
+    const dim3 jg((unsigned)items, 2);
+    if (a.d == 64) window_join_kernel<64><<<jg, 256, 0, st>>>(a, (__nv_bfloat16 *)O, tok, nblk, starts);
+    else window_join_kernel<128><<<jg, 256, 0, st>>>(a, (__nv_bfloat16 *)O, tok, nblk, starts);
+    return cudaGetLastError();
+}
+
+TcPlan tc_plan(const LocArgs &a, long long most_keys) {
+    const int tok = MR / a.G, nblk = (a.max_q + 2 * tok - 1) / (2 * tok);
+    const long long blocks = (long long)a.B * nblk, items = blocks * a.Hkv;
+    TcPlan p{};
+    // 16 items per SM and more balance by themselves, and items of fewer than 16 key tiles are not worth their cuts and
+    // the second launch (300 items of 6 tiles: 36 us whole, 92 us shared; 136 of 113 to 256: 833 us and 509 us).  The
+    // scan of the blocks' lengths, one warp per CTA, is kept to 1024 blocks.
+    p.shares = items > 0 && items < 16 * 148 && blocks <= 1024 && most_keys >= 16 * BK;
+    if (p.shares) {
+        p.starts = (size_t)(blocks + 2) * sizeof(long long);
+        // two slots (first and last item) for each CTA that can get a share
+        long long ctas = items * (most_keys / BK + 3) / SHARE_LEAST + 1;
+        if (ctas > 148) ctas = 148;
+        p.opart = (size_t)(2 * ctas) * 2 * MR * a.d * sizeof(float);
+        p.lpart = (size_t)(2 * ctas) * 2 * MR * sizeof(float);
+    }
+    return p;
 }
 
 }  // namespace local

@@ -75,6 +75,13 @@ def test_window_tokens_over_a_cache(Tq, past, window, sinks):
     _forward(F32 if Tq < 9 else BF, 64, 4, 1, 1, Tq, n, n + 70, past, window, sinks)
 
 
+@pytest.mark.parametrize("B", [1, 9, 40, 160])
+def test_window_many_items(B):
+    """Several items per CTA, some with one row tile and some with two, shared between CTAs or whole."""
+    _forward(BF, 64, 16, 8, B, 130, 130, 131, 0, 40, 2)
+    _forward(BF, 128, 8, 8, B, 150, 450, 450, 300, 0, 0)
+
+
 @pytest.mark.parametrize("simt", [False, True])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_window_rows_that_see_nothing(dt, simt):
@@ -184,6 +191,12 @@ def test_window_backward_of_a_chunk(dt):
     _backward(dt, 64, 4, 2, 1, 40, 30, 33, 400, 10, 3)         # only sinks are seen
     _backward(dt, 128, 8, 2, 1, 300, 300, 300, 0, 50, 300)     # every key is a sink
     _backward(dt, 64, 8, 2, 2, 333, 333, 340, 0, 77, 5, scale=0.2, simt=True)
+
+
+@pytest.mark.parametrize("B", [1, 9, 40])
+def test_window_backward_many_items(B):
+    _backward(BF, 64, 16, 8, B, 130, 130, 131, 0, 40, 2)
+    _backward(BF, 128, 8, 8, B, 150, 150, 150, 0, 0, 0)
 
 
 def test_window_backward_against_differences():
