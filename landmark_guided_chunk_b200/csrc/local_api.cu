@@ -364,6 +364,11 @@ hsa_status_t hsa_rope_init(hsa_rope_t *r) {
 
 namespace {
 
+hsa_status_t check_head_count(int heads) {
+    if (heads > 16383) return fail(HSA_ERR_UNSUPPORTED, "%d heads in one call (max 16383)", heads);
+    return HSA_OK;
+}
+
 hsa_status_t rope_args(const hsa_rope_t *rope, int d, RopeArgs *r) {
     if (!rope) return fail(HSA_ERR_INVALID_ARG, "rope is NULL");
     if (rope->rot < 2 || rope->rot > d || rope->rot % 2)
@@ -397,6 +402,7 @@ hsa_status_t hsa_rope(const hsa_rope_t *rope, const hsa_window_t *prob, const in
     HSA_TRY(shape_of(&pr, &a));
     RopeArgs r;
     HSA_TRY(rope_args(rope, a.d, &r));
+    HSA_TRY(check_head_count((Q ? a.H : 0) + (K ? a.Hkv : 0)));
     const bool rows = a.rows > 0;
     if (rows && !Q && !K) return fail(HSA_ERR_INVALID_ARG, "Q and K are both NULL");
     HSA_TRY(need(Q, Q != nullptr, "Q"));
@@ -419,6 +425,7 @@ hsa_status_t hsa_paged_append(const hsa_paged_t *prob, const hsa_rope_t *rope, c
     HSA_TRY(shape_of(prob, &a));
     RopeArgs r;
     if (rope) HSA_TRY(rope_args(rope, a.d, &r));
+    HSA_TRY(check_head_count((Q ? a.H : 0) + 2 * a.Hkv));
     const bool any = a.rows > 0 && a.B > 0;
     HSA_TRY(need(k_new, any, "k_new"));
     HSA_TRY(need(v_new, any, "v_new"));

@@ -26,6 +26,7 @@ __all__ = ["make_rope", "rope", "window_workspace", "window_attend", "window_bac
 _DT = {torch.float32: _native.HSA_F32, torch.bfloat16: _native.HSA_BF16}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 _byref = ctypes.byref
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream(index).cuda_stream without the objects around it
 
 
 def _dtype(t):
@@ -37,30 +38,37 @@ def _dtype(t):
 
 def _check(like, *ts):
     """CUDA, contiguous, on one device, of one dtype (None is passed over)."""
-    dev, dt = like.device, like.dtype
-    for t in (like,) + ts:
+    dev, dt = like.get_device(), like.dtype
+    if dev >= 0 and like.is_contiguous():
+        for t in ts:
+            if t is not None and (t.get_device() != dev or t.dtype is not dt or not t.is_contiguous()):
+                break
+        else:
+            return
+    for t in (like,) + ts:      # something is wrong: say what
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("all tensors must be CUDA tensors")
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors on {like.device} and {t.device}")
         if t.dtype != dt:
             raise TypeError(f"tensors of {dt} and {t.dtype}")
 
 
-def _ints(like, **ts):
-    for name, t in ts.items():
-        if t.dtype != torch.int32:
+def _ints(like, *names_tensors):
+    dev = like.get_device()
+    for name, t in names_tensors:
+        if t.dtype is not torch.int32:
             raise TypeError(f"{name} must be int32, got {t.dtype}")
-        if t.device != like.device or not t.is_contiguous():
+        if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and on {like.device}")
 
 
 def _shape(name, t, want):
-    if t is not None and tuple(t.shape) != tuple(want):
+    if t is not None and t.shape != want:
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(want)}")
 
 
@@ -71,12 +79,12 @@ def _p(t):
 def _call(name, like, *args):
     """One library call on the current stream of `like`'s device, with that device current."""
     fn = getattr(_native.lib(), name)
-    index = like.device.index
+    index = like.get_device()
     if torch.cuda.current_device() == index:
-        status = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+            status = fn(*args, _raw_stream(index))
     if status:
         _native.check(status, name)
 
@@ -118,7 +126,7 @@ def rope(r: hsa_rope_t, Q=None, K=None, pos0: int = 0, pos=None, inverse: bool =
         if H % Hkv:   # the heads are independent here: any two counts are fine, each in its own launch
             return (rope(r, Q, None, pos0, pos, inverse, Q_out), rope(r, None, K, pos0, pos, inverse, None, K_out))
     if pos is not None:
-        _ints(x, pos=pos)
+        _ints(x, ("pos", pos))
         _shape("pos", pos, (B, T))
     if Q is not None and Q_out is None:
         Q_out = torch.empty_like(Q)
@@ -215,7 +223,7 @@ def paged_append(k_new, v_new, K_pages, V_pages, q_start, kv_len, table, Q=None,
     rope (make_rope) K is rotated to its position on the way, and Q [rows,H,d] too.  Returns Q_out (Q rotated; a
     new tensor unless given; rows behind the last sequence are not written), or None without Q."""
     _check(k_new, v_new, K_pages, V_pages, Q, Q_out)
-    _ints(k_new, q_start=q_start, kv_len=kv_len, table=table)
+    _ints(k_new, ("q_start", q_start), ("kv_len", kv_len), ("table", table))
     rows, Hkv, d = k_new.shape
     npages, page, B = K_pages.shape[0], K_pages.shape[1], table.shape[0]
     _shape("v_new", v_new, k_new.shape)
@@ -245,7 +253,7 @@ def paged_attend(Q, K_pages, V_pages, q_start, kv_len, table, max_q=None, max_kv
     rows, and what a table row can hold); the closer they are, the better the work is split.  Returns O; rows
     behind the last sequence are not written."""
     _check(Q, K_pages, V_pages, O)
-    _ints(Q, q_start=q_start, kv_len=kv_len, table=table)
+    _ints(Q, ("q_start", q_start), ("kv_len", kv_len), ("table", table))
     rows, H, d = Q.shape
     B = table.shape[0]
     _shape("V_pages", V_pages, K_pages.shape)

@@ -142,6 +142,10 @@ def test_rope_call_refusals():
     for r in (hsa.make_rope(128), hsa_rope_t()):       # wider than the head; never set up
         assert L.hsa_rope(ctypes.byref(r), p, None, 0, PTR, PTR, PTR, PTR, None) == INVALID
     r = ctypes.byref(hsa.make_rope(64))
+    wide = ctypes.byref(_window(d=64, H=16000, Hkv=1000))
+    assert L.hsa_rope(r, wide, None, 0, PTR, PTR, PTR, PTR, None) == UNSUPPORTED
+    wide = ctypes.byref(_paged(d=64, H=16000, Hkv=1000))
+    assert L.hsa_paged_append(wide, r, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, BIG, None) == UNSUPPORTED
     assert L.hsa_rope(None, p, None, 0, PTR, PTR, PTR, PTR, None) == INVALID
     assert L.hsa_rope(r, None, None, 0, PTR, PTR, PTR, PTR, None) == INVALID
     bad = hsa_rope_t(64, 0, 9, 0, 1e4, 1.0)
