@@ -113,19 +113,52 @@ __host__ __device__ __forceinline__ void split_range(int nt, int nsplit, int s, 
     *i1 = *i0 + per < nt ? *i0 + per : nt;
 }
 
-// Backward: the key tiles that hold sinks are seen by every later query.  Their
-// far part (queries beyond the window) is cut into chunks of `far_q` tokens, each
-// a work item of its own that writes fp32 partials.
+// Backward, dK and dV: the work items of a key tile.  The queries inside its window are
+// cut into nwin chunks of win_q tokens (1 unless few tiles would leave SMs idle); the key tiles
+// that hold sinks are seen by every later query too, in nfar more chunks of far_q tokens.  A
+// tile of several items is written as fp32 partials, one slot per item, that bwd_join_kernel adds
+// in slot order.
 struct BwdArgs {
     LocArgs a;                       // contiguous view; a.lse = the forward's
     int nkt;                         // key tiles over Tkv
+    int nwin, win_q;
     int nst;                         // key tiles that hold sinks and have a far part (0: none)
-    int nfar, far_q;                 // far chunks per such tile, tokens per chunk
+    int nfar, far_q;
+    int npt;                         // key tiles written as partials: the first npt
     float *D;                        // [B][Tq][H] row sums of dO o O
-    float *part;                     // [2 (dK, dV)][nfar + 1][B][Hkv][nst * BK][d]
+    float *part;                     // [2 (dK, dV)][nwin + nfar][B][Hkv][npt * BK][d]
 };
 
-long long most_keys(const LocArgs &a, int tok);   // that `tok` consecutive queries can see, at most
+// Work item x (of nkt * nwin + nst * nfar): its key tile, its slot and its query tokens [ta, tb).
+struct KvRange {
+    int kt, slot, ta, tb;
+};
+__host__ __device__ __forceinline__ KvRange kv_range(const BwdArgs &w, const Seq &s, int x, int bk) {
+    KvRange r;
+    const bool far = x >= w.nkt * w.nwin;
+    int c;
+    if (far) {
+        x -= w.nkt * w.nwin;
+        r.kt = x / w.nfar;
+        c = x % w.nfar;
+        r.slot = w.nwin + c;
+    } else {
+        r.kt = x / w.nwin;
+        r.slot = c = x % w.nwin;
+    }
+    const int u0 = r.kt * bk, ul = (u0 + bk < s.kv ? u0 + bk : s.kv) - 1;
+    const long long n = s.n, t0 = u0 > s.pos0 ? u0 - s.pos0 : 0;
+    // first token beyond the window of every key of the tile
+    long long edge = w.a.window < INT32_MAX ? (long long)ul + w.a.window - s.pos0 : n;
+    edge = edge < 0 ? 0 : edge > n ? n : edge;
+    long long lo = far ? (edge > t0 ? edge : t0) : t0;
+    const long long hi = far ? n : edge, step = far ? w.far_q : w.win_q;
+    lo += c * step;
+    const long long end = lo + step < hi ? lo + step : hi;
+    r.ta = (int)(lo < n ? lo : n);
+    r.tb = (int)(end > r.ta ? end : r.ta);
+    return r;
+}
 
 struct LocPlan {
     bool tc, few;          // forward path: tcgen05 tiles, few-row kernel; neither: CUDA-core tiles
@@ -136,7 +169,7 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt);
 
 struct BwdPlan {
     bool tc;
-    int nkt, nst, nfar, far_q, bk;
+    int nkt, nwin, win_q, nst, nfar, far_q, npt, bk;
     size_t D, part, extra, total;
 };
 BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt);

@@ -196,22 +196,36 @@ BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt) {
     p.tc = !simt && bwd_tc_supported(a, dtype);
     p.bk = p.tc ? 128 : 64;
     p.nkt = ceil_div(a.max_kv, p.bk);
+    // few key tiles: their rows are shared between CTAs as well, two row tiles (tcgen05: four) each at least
+    const int tok = 64 / a.G;                      // both paths' row tiles are 64 rows
+    long long range = a.window < INT32_MAX ? (long long)a.window + p.bk : a.max_q;
+    if (range > a.max_q) range = a.max_q;
+    const long long items = (long long)a.B * a.Hkv * p.nkt, want = p.tc ? SMS : 2 * SMS;
+    p.nwin = 1;
+    if (items > 0 && items < want) {
+        long long n = want / items, most = range / ((p.tc ? 4 : 2) * tok);
+        if (n > most) n = most;
+        if (n > 16) n = 16;
+        if (n > 1) p.nwin = (int)n;
+    }
+    p.win_q = range > 0 ? ceil_div(ceil_div(range, p.nwin), tok) * tok : 1;
     const int sinks = a.sinks < a.max_kv ? a.sinks : a.max_kv;
     if (a.window < INT32_MAX && sinks > 0 && a.max_q > 0 && (long long)a.q_pos0 + a.max_q - 1 >= a.window) {
         p.nst = ceil_div(sinks, p.bk);
-        // chunks about as long as a window's range of queries, at most 64 of them over all sink tiles
+        // the far rows of a sink tile in chunks as long as the others, at most 64 of them over all sink tiles
         const int most = 64 / p.nst > 1 ? 64 / p.nst : 1;
-        long long fq = (long long)a.window + p.bk;
+        long long fq = p.win_q;
         if (fq < ceil_div(a.max_q, most)) fq = ceil_div(a.max_q, most);
         if (fq > a.max_q) fq = a.max_q;
         p.far_q = (int)fq;
         p.nfar = ceil_div(a.max_q, fq);
     }
+    p.npt = p.nwin > 1 ? p.nkt : p.nst;
     size_t off = HDR;
     p.D = off;
     off += align256((size_t)a.rows * a.H * sizeof(float));
     p.part = off;
-    off += align256(2 * (size_t)(p.nfar + 1) * a.B * a.Hkv * p.nst * p.bk * a.d * sizeof(float));
+    if (p.npt > 0) off += align256(2 * (size_t)(p.nwin + p.nfar) * a.B * a.Hkv * p.npt * p.bk * a.d * sizeof(float));
     p.total = off;
     return p;
 }
@@ -281,6 +295,9 @@ hsa_status_t hsa_window_backward(const hsa_window_t *prob, const void *Q, const 
     BwdArgs w{};
     w.a = a;
     w.nkt = pl.nkt;
+    w.nwin = pl.nwin;
+    w.win_q = pl.win_q;
+    w.npt = pl.npt;
     w.nst = pl.nst;
     w.nfar = pl.nfar;
     w.far_q = pl.far_q;

@@ -496,9 +496,9 @@ struct __align__(16) KvBars {
 static_assert(offsetof(KvBars, lse2) % 16 == 0 && offsetof(KvBars, dd) % 16 == 0, "vector loads");
 
 struct KvItem {
-    int b, j, kt, far, u0, ta, tb;   // key tile, far chunk (-1: the window's rows), first key, query tokens [ta, tb)
+    int b, j, kt, slot, u0, ta, tb;   // key tile, its partials' slot, first key, query tokens [ta, tb)
     Seq s;
-    int nt;                          // row tiles
+    int nt;                           // row tiles
 };
 
 __device__ __forceinline__ KvItem kv_item(const BwdArgs &w, int idx, int tok) {
@@ -507,28 +507,14 @@ __device__ __forceinline__ KvItem kv_item(const BwdArgs &w, int idx, int tok) {
     it.j = idx % a.Hkv;
     idx /= a.Hkv;
     it.b = idx % a.B;
-    it.kt = idx / a.B;   // early keys first: without a window they are seen by the most rows
-    it.far = -1;
-    if (it.kt >= w.nkt) {
-        it.far = (it.kt - w.nkt) % w.nfar;
-        it.kt = (it.kt - w.nkt) / w.nfar;
-    }
     it.s = seq_of(a, it.b);
-    it.u0 = it.kt * MR;
-    const int ul = min(it.u0 + MR, it.s.kv) - 1;
-    it.ta = max(0, it.u0 - it.s.pos0);
-    it.tb = it.s.n;
-    if (a.window < INT32_MAX) {
-        const long long edge = (long long)ul + a.window - it.s.pos0;   // first token beyond the window of every key
-        if (it.far < 0) {
-            it.tb = (int)max(0ll, min((long long)it.s.n, edge));
-        } else {
-            const long long f0 = max(0ll, max((long long)it.ta, edge));
-            it.ta = (int)min((long long)it.s.n, f0 + (long long)it.far * w.far_q);
-            it.tb = (int)min((long long)it.s.n, f0 + (long long)(it.far + 1) * w.far_q);
-        }
-    }
-    it.nt = it.tb > it.ta ? (it.tb - it.ta + tok - 1) / tok : 0;
+    const KvRange r = kv_range(w, it.s, idx / a.B, MR);   // early keys first: without a window the most rows see them
+    it.kt = r.kt;
+    it.slot = r.slot;
+    it.u0 = r.kt * MR;
+    it.ta = r.ta;
+    it.tb = r.tb;
+    it.nt = (it.tb - it.ta + tok - 1) / tok;
     return it;
 }
 
@@ -643,14 +629,14 @@ __global__ void __launch_bounds__(NTK, 1)
                 if (!(ok = mbar_wait(&bar->acc_full, ni++ & 1, abort, status))) break;
                 tc_fence_after();
             }
-            // this warpgroup's quarter of the columns of dK and dV: the outputs, or fp32 partials of a sink tile
+            // this warpgroup's quarter of the columns of dK and dV: the outputs, or fp32 partials
             constexpr int QC = D / 4;
             const int col = (warp >> 2) * QC;
-            const bool part = it.kt < w.nst;
-            const long long psz = (long long)a.B * a.Hkv * w.nst * MR * D;
-            const long long prow = part ? (((long long)it.b * a.Hkv + it.j) * w.nst * MR + u) * D + col : 0;
-            float *pk = part ? w.part + (it.far + 1) * psz + prow : nullptr;
-            float *pv = part ? pk + (w.nfar + 1) * psz : nullptr;
+            const bool part = it.kt < w.npt;
+            const long long psz = (long long)a.B * a.Hkv * w.npt * MR * D;
+            const long long prow = part ? (((long long)it.b * a.Hkv + it.j) * w.npt * MR + u) * D + col : 0;
+            float *pk = part ? w.part + it.slot * psz + prow : nullptr;
+            float *pv = part ? pk + (w.nwin + w.nfar) * psz : nullptr;
             const long long at = live ? (((long long)it.b * a.Tcap + u) * a.Hkv + it.j) * D + col : 0;
             if (it.nt > 0) {
                 put<QC>(lane_off + 256 + col, 1.f, dV + at, pv, live);
@@ -901,7 +887,7 @@ cudaError_t launch_bwd_tc(const BwdArgs &w, const void *Q, const void *K, const 
     if (e == cudaSuccess) e = make_tmap_3d(&mk, K, kd, ks, kb);
     if (e == cudaSuccess) e = make_tmap_3d(&mv, V, kd, ks, kb);
     if (e != cudaSuccess) return e;
-    const long long nq = (long long)a.B * nblk * a.Hkv, nk = (long long)a.B * (w.nkt + w.nst * w.nfar) * a.Hkv;
+    const long long nq = (long long)a.B * nblk * a.Hkv, nk = (long long)a.B * (w.nkt * w.nwin + w.nst * w.nfar) * a.Hkv;
     auto go = [&](auto dq, auto dkv, int tile) {
         const size_t s1 = 1024 + (size_t)(2 + (KST + VST) / 2) * tile + sizeof(DqBars);
         const size_t s2 = 1024 + (size_t)(2 + RST) * tile + sizeof(KvBars);   // a row tile of Q and dO: one tile's bytes

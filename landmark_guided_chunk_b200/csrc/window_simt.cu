@@ -347,8 +347,7 @@ __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restr
 }
 
 // dK, dV of one key tile: over the rows of every query token that sees it.
-// Work item x: tiles 0 .. nkt-1 with the queries inside their window, then the
-// far chunks of the sink tiles (fp32 partials, joined by bwd_join_kernel).
+// Work item x: see kv_range.
 template <typename T, int D>
 __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__restrict__ Q, const T *__restrict__ K,
                                                       const T *__restrict__ V, const T *__restrict__ dO,
@@ -359,25 +358,9 @@ __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__rest
           *sP = sG + BM * (D + 4), *sS = sP + BM * PP;
     const int b = blockIdx.z, j = blockIdx.y;
     const Seq s = seq_of(a, b);
-    int kt = blockIdx.x, far = -1;
-    if (kt >= w.nkt) {
-        far = (kt - w.nkt) % w.nfar;
-        kt = (kt - w.nkt) / w.nfar;
-    }
-    const int u0 = kt * BN, ul = min(u0 + BN, s.kv) - 1;
-    const bool sink = kt < w.nst;
-    // query tokens [ta, tb): from the tile's first key on; inside the window of its last key, or the far chunk
-    int ta = max(0, u0 - s.pos0), tb = s.n;
-    if (a.window < INT32_MAX) {
-        const long long edge = (long long)ul + a.window - s.pos0;   // first token beyond the window of every key
-        if (far < 0)
-            tb = (int)max(0ll, min((long long)s.n, edge));
-        else {
-            const long long f0 = max(0ll, max((long long)ta, edge));
-            ta = (int)min((long long)s.n, f0 + (long long)far * w.far_q);
-            tb = (int)min((long long)s.n, f0 + (long long)(far + 1) * w.far_q);
-        }
-    }
+    const KvRange it = kv_range(w, s, blockIdx.x, BN);
+    const int u0 = it.kt * BN, ta = it.ta, tb = it.tb;
+    const bool part = it.kt < w.npt;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     auto src = [&](int r) -> long long {
         return u0 + r < s.kv ? (kv_row(a, b, u0 + r) * a.Hkv + j) * D : -1;
@@ -425,7 +408,7 @@ __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__rest
         acc_tile<D, D + 4, true>(sP, sG, ty, tx, gv);
         acc_tile<D, D + 4, true>(sS, sQ, ty, tx, gk);
     }
-    const long long psz = (long long)a.B * a.Hkv * w.nst * BN * D;   // one slot of partials
+    const long long psz = (long long)a.B * a.Hkv * w.npt * BN * D;   // one slot of partials
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int u = u0 + ty * 4 + i;
@@ -439,9 +422,9 @@ __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__rest
                 k4[x] = gk[i][4 * c + x] * a.scale;
                 v4[x] = gv[i][4 * c + x];
             }
-            if (sink) {
-                const long long at = (((long long)b * a.Hkv + j) * w.nst * BN + u) * D + col;
-                float *pk = w.part + (far + 1) * psz + at, *pv = pk + (w.nfar + 1) * psz;
+            if (part) {
+                const long long at = (((long long)b * a.Hkv + j) * w.npt * BN + u) * D + col;
+                float *pk = w.part + it.slot * psz + at, *pv = pk + (w.nwin + w.nfar) * psz;
                 store4<float>(pk, k4[0], k4[1], k4[2], k4[3]);
                 store4<float>(pv, v4[0], v4[1], v4[2], v4[3]);
             } else {
@@ -453,20 +436,21 @@ __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__rest
     }
 }
 
-// dK, dV of the sink tiles: their partials summed in slot order (window part
-// first, then the far chunks), rounded once.  One thread per four elements.
+// dK, dV of the tiles written as partials, summed in slot order (the window's chunks, then
+// the far ones of sink tiles) and rounded once.  One thread per four elements.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) bwd_join_kernel(BwdArgs w, int bk, T *__restrict__ dK, T *__restrict__ dV) {
     const LocArgs &a = w.a;
-    const long long psz = (long long)a.B * a.Hkv * w.nst * bk * D;
+    const long long psz = (long long)a.B * a.Hkv * w.npt * bk * D;
     const long long e = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
     if (e >= psz) return;
-    const int u = (int)(e / D % (w.nst * bk));
-    const long long bj = e / D / (w.nst * bk);
+    const int u = (int)(e / D % (w.npt * bk));
+    const long long bj = e / D / (w.npt * bk);
     if (u >= a.max_kv) return;
-    const float *src = w.part + (blockIdx.y ? (w.nfar + 1) * psz : 0) + e;
+    const float *src = w.part + (blockIdx.y ? (w.nwin + w.nfar) * psz : 0) + e;
+    const int slots = w.nwin + (u / bk < w.nst ? w.nfar : 0);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i <= w.nfar; ++i) {
+    for (int i = 0; i < slots; ++i) {
         const float4 v = *reinterpret_cast<const float4 *>(src + i * psz);
         s.x += v.x;
         s.y += v.y;
@@ -505,7 +489,7 @@ cudaError_t bwd(const BwdArgs &w, const void *Q, const void *K, const void *V, c
         simt_dq_kernel<T, D><<<dim3((w.a.max_q + tok - 1) / tok, w.a.Hkv, w.a.B), NT, s1, st>>>(
             w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dQ);
     if (w.nkt > 0)
-        simt_dkv_kernel<T, D><<<dim3(w.nkt + w.nst * w.nfar, w.a.Hkv, w.a.B), NT, s2, st>>>(
+        simt_dkv_kernel<T, D><<<dim3(w.nkt * w.nwin + w.nst * w.nfar, w.a.Hkv, w.a.B), NT, s2, st>>>(
             w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dK, (T *)dV);
     return cudaGetLastError();
 }
@@ -560,8 +544,8 @@ cudaError_t launch_bwd_simt(const BwdArgs &w, int dtype, const void *Q, const vo
 }
 
 cudaError_t launch_bwd_join(const BwdArgs &w, int bk, int dtype, void *dK, void *dV, cudaStream_t st) {
-    if (w.nst == 0) return cudaSuccess;
-    const long long psz = (long long)w.a.B * w.a.Hkv * w.nst * bk * w.a.d;
+    if (w.npt == 0) return cudaSuccess;
+    const long long psz = (long long)w.a.B * w.a.Hkv * w.npt * bk * w.a.d;
     const dim3 grid((unsigned)((psz / 4 + 255) / 256), 2);
     if (dtype == HSA_F32) {
         if (w.a.d == 64) bwd_join_kernel<float, 64><<<grid, 256, 0, st>>>(w, bk, (float *)dK, (float *)dV);

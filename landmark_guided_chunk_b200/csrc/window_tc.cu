@@ -757,10 +757,12 @@ TcPlan tc_plan(const LocArgs &a, long long most_keys) {
     const int tok = MR / a.G, nblk = (a.max_q + 2 * tok - 1) / (2 * tok);
     const long long blocks = (long long)a.B * nblk, items = blocks * a.Hkv;
     TcPlan p{};
-    // 16 items per SM and more balance by themselves, and items of fewer than 16 key tiles are not worth their cuts and
-    // the second launch (300 items of 6 tiles: 36 us whole, 92 us shared; 136 of 113 to 256: 833 us and 509 us).  The
-    // scan of the blocks' lengths, one warp per CTA, is kept to 1024 blocks.
-    p.shares = items > 0 && items < 16 * 148 && blocks <= 1024 && most_keys >= 16 * BK;
+    // Shares where whole items would leave SMs idle: fewer than two items per SM, or 16 where the lengths are not
+    // known here.  More items balance by themselves and run faster whole, since neighbouring CTAs then read the same
+    // keys (2048 items of 33 tiles: 890 us whole, 1148 us shared); items of fewer than 16 key tiles are not worth
+    // their cuts and the second launch (300 of 6 tiles: 35 us whole, 53 us and the join shared; but 136 of 113 to 256: 833 us and 492 us).
+    // The scan of the blocks' lengths, one warp per CTA, is kept to 1024 blocks.
+    p.shares = items > 0 && items < (a.paged ? 16 : 2) * 148 && blocks <= 1024 && most_keys >= 16 * BK;
     if (p.shares) {
         p.starts = (size_t)(blocks + 2) * sizeof(long long);
         // two slots (first and last item) for each CTA that can get a share
