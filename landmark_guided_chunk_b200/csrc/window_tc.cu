@@ -34,7 +34,8 @@ constexpr float RESCALE = 8.f;   // growth of the maximum (log2) that is let pas
 template <int D> struct Cfg {
     static constexpr int NBX = D / 64;                 // 64-column boxes per row
     static constexpr int TILE = 128 * D * 2;           // bytes of a Q, K or V tile
-    static constexpr int NST = D == 128 ? 3 : 8;       // K/V ring stages
+    static constexpr int QB = 2;                       // buffers of the two Q tiles
+    static constexpr int NST = D == 128 ? 3 : 8;       // K/V ring stages (one Q buffer and 5 stages: 908 -> 927 us)
 };
 
 struct Share {
@@ -149,12 +150,10 @@ struct Walk {
     }
 };
 
-// Start of CTA c's share in the row of `total` tiles that `ctas` CTAs divide.
-__device__ __forceinline__ long long share_start(long long total, int ctas, int c) { return total * c / ctas; }
 constexpr int SHARE_LEAST = 8;   // key tiles per CTA at least: a cut's partials and their join cost about four
 
 // One warp: the sum of all blocks' tiles times kv heads, and this CTA's share of them.  CTA 0 leaves the blocks'
-// starts in `starts` (int64 [blocks + 1], then the number of CTAs) for the join.
+// starts in `starts` (int64 [blocks + 1], then the tiles per CTA) for the join.
 __device__ __forceinline__ Share find_share(const LocArgs &a, int tok, int nblk, long long *starts) {
     const int lane = threadIdx.x & 31, nb = a.B * nblk;
     auto weight_of = [&](int g) -> int {
@@ -165,10 +164,10 @@ __device__ __forceinline__ Share find_share(const LocArgs &a, int tok, int nblk,
     };
     long long total = 0;
     for (int g0 = 0; g0 < nb; g0 += 32) total += __reduce_add_sync(FULL, (unsigned)weight_of(g0 + lane));
-    const int ctas = (int)max(1ll, min((long long)gridDim.x, total / SHARE_LEAST));
+    const long long per = max((long long)SHARE_LEAST, (total + gridDim.x - 1) / gridDim.x);   // tiles per CTA
     const int c = blockIdx.x;
     Share sh{0, 0, 0, 0};
-    const long long s0 = share_start(total, ctas, c), s1 = share_start(total, ctas, c + 1);
+    const long long s0 = min(total, c * per), s1 = min(total, s0 + per);
     long long at = 0;
     for (int g0 = 0; g0 < nb; g0 += 32) {
         const int wl = weight_of(g0 + lane);
@@ -180,18 +179,18 @@ __device__ __forceinline__ Share find_share(const LocArgs &a, int tok, int nblk,
         }
         const long long before = at + inc - wl;
         if (c == 0 && g0 + lane < nb) starts[g0 + lane] = before;
-        if (c < ctas && wl > 0 && before <= s0 && s0 < before + wl) {
-            const int per = wl / a.Hkv, off = (int)(s0 - before);
+        if (s0 < s1 && wl > 0 && before <= s0 && s0 < before + wl) {
+            const int tiles = wl / a.Hkv, off = (int)(s0 - before);
             sh.g = g0 + lane;
-            sh.j = off / per;
-            sh.i = off % per;
+            sh.j = off / tiles;
+            sh.i = off % tiles;
             sh.left = (int)(s1 - s0);
         }
         at += __shfl_sync(FULL, inc, 31);
     }
     if (c == 0 && lane == 0) {
         starts[nb] = total;
-        starts[nb + 1] = ctas;
+        starts[nb + 1] = per;
     }
     sh.g = (int)__reduce_max_sync(FULL, (unsigned)sh.g);   // one lane has found it, the others hold zeros
     sh.j = (int)__reduce_max_sync(FULL, (unsigned)sh.j);
@@ -200,29 +199,26 @@ __device__ __forceinline__ Share find_share(const LocArgs &a, int tok, int nblk,
     return sh;
 }
 
-// Joins the partials of the items that the shares cut: O = sum exp(lse_i - lse) O_i, in order of the pieces.  One
-// block per (item, row tile).
+constexpr int JOIN_ROWS = 4;   // blocks per row tile
+
+// Joins the partials of the items that the shares cut: O = sum exp(lse_i - lse) O_i, in order of the pieces.  Four
+// blocks per (item, row tile).
 template <int D>
 __global__ void __launch_bounds__(256)
     window_join_kernel(const __grid_constant__ LocArgs a, __nv_bfloat16 *__restrict__ O, int tok, int nblk, const long long *starts) {
-    const int nb = a.B * nblk, g = blockIdx.x / a.Hkv, j = blockIdx.x % a.Hkv, t = blockIdx.y;
-    const long long total = starts[nb], s = starts[g], e = starts[g + 1];
-    const int ctas = (int)starts[nb + 1];
+    const int nb = a.B * nblk, g = blockIdx.x / a.Hkv, j = blockIdx.x % a.Hkv;
+    const int t = blockIdx.y / JOIN_ROWS, r0 = blockIdx.y % JOIN_ROWS * (MR / JOIN_ROWS);   // row tile, first of its rows here
+    const long long s = starts[g], e = starts[g + 1], per = starts[nb + 1];
     if (e == s) return;
-    const long long per = (e - s) / a.Hkv, i0 = s + j * per, i1 = i0 + per;
-    // CTA of a tile: the c with share_start(c) <= tile < share_start(c + 1)
-    auto cta_of = [&](long long x) -> int {
-        int c = (int)(x * ctas / total);
-        while (c + 1 < ctas && share_start(total, ctas, c + 1) <= x) ++c;
-        while (share_start(total, ctas, c) > x) --c;
-        return c;
-    };
+    const long long tiles = (e - s) / a.Hkv, i0 = s + j * tiles, i1 = i0 + tiles;
+    // CTA of a tile (exact: both numbers are far below 2^53)
+    auto cta_of = [&](long long x) -> int { return (int)((double)x / (double)per); };
     const int c0 = cta_of(i0), pieces = cta_of(i1 - 1) - c0 + 1;
     if (pieces == 1) return;
     // the piece is its CTA's first item unless that CTA started before it
     __shared__ int slot[148];
     if (threadIdx.x < pieces)
-        slot[threadIdx.x] = 2 * (c0 + threadIdx.x) + (share_start(total, ctas, c0 + threadIdx.x) >= i0 ? 0 : 1);
+        slot[threadIdx.x] = 2 * (c0 + (int)threadIdx.x) + ((c0 + (int)threadIdx.x) * per >= i0 ? 0 : 1);
     __syncthreads();
     Item it;
     block_of(a, g, tok, nblk, &it);
@@ -230,7 +226,7 @@ __global__ void __launch_bounds__(256)
     constexpr int TPR = D / 4, RPB = 256 / TPR;
     const int col = threadIdx.x % TPR * 4;
 #pragma unroll 2
-    for (int r = threadIdx.x / TPR; r < tok * a.G; r += RPB) {
+    for (int r = r0 + threadIdx.x / TPR; r < min(r0 + MR / JOIN_ROWS, tok * a.G); r += RPB) {
         const int token = it.t0 + t * tok + r / a.G;
         if (token >= it.s.n) continue;
         const long long rt = t * MR + r;
@@ -268,15 +264,15 @@ __global__ void __launch_bounds__(NT, 1)
     typedef Cfg<D> C;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = base;                       // 2 buffers x 2 tiles: Q, then the item's output
-    uint8_t *sKV = base + 4 * C::TILE;        // NST tiles
+    uint8_t *sQ = base;                       // QB buffers x 2 tiles: Q, then the item's output
+    uint8_t *sKV = base + 2 * C::QB * C::TILE;   // NST tiles
     Bars *bar = reinterpret_cast<Bars *>(sKV + C::NST * C::TILE);
     volatile int *abort = &bar->abort;
     uint32_t *status = a.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // rows that no box covers (G does not divide 128) stay zero
-    for (int i = threadIdx.x; i < 4 * C::TILE / 16; i += NT) reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 2 * C::QB * C::TILE / 16; i += NT) reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             for (int x = 0; x < 2; ++x) {
@@ -439,7 +435,7 @@ __global__ void __launch_bounds__(NT, 1)
             const long long prow = (long long)it.slot * 2 * MR + t * MR + r;
             // whole tiles go out by TMA from the Q buffer, which no product reads any more
             const bool whole = it.slot < 0 && it.t0 + (t + 1) * tok <= it.s.n;
-            uint8_t *stage = sQ + ((na & 1) * 2 + t) * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
+            uint8_t *stage = sQ + (na % C::QB * 2 + t) * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
@@ -534,7 +530,7 @@ __global__ void __launch_bounds__(NT, 1)
                         ++nkv;
                         if (kv == 0 && i == it.i0) {
                             // the item's query tiles, into the buffer that the item before last has left
-                            const int x = na++ & 1;
+                            const int x = na++ % C::QB;
                             for (int t = 0; t < it.ntile && ok; ++t) {
                                 const uint32_t bit = 1u << (2 * x + t);
                                 if ((qused & bit) &&
@@ -571,7 +567,7 @@ __global__ void __launch_bounds__(NT, 1)
             Item it;
             for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
-                const int nt = it.i1 - it.i0, x = na++ & 1;   // key tiles, Q buffer
+                const int nt = it.i1 - it.i0, x = na++ % C::QB;   // key tiles, Q buffer
                 // ring stages of K and V of tile i and of K of tile i + 1
                 auto after = [](uint32_t st) { return st + 1 == C::NST ? 0u : st + 1; };
                 auto wait_kv = [&](uint32_t st) {
@@ -662,7 +658,7 @@ __global__ void __launch_bounds__(NT, 1)
             Item it;
             for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
-                const int x = na++ & 1;
+                const int x = na++ % C::QB;
                 for (int t = 0; t < it.ntile; ++t) {
                     if (!(ok = mbar_wait(&bar->out_full[t], par >> t & 1, abort, status))) break;
                     par ^= 1u << t;
@@ -737,17 +733,17 @@ cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void
     if (e != cudaSuccess) return e;
     // shares: every SM may get one, however few the items
     const int grid = items < 148 && !starts ? (int)items : 148;
-    auto go = [&](auto kern, int tile, int nst) {
-        const size_t smem = 1024 + (size_t)(4 + nst) * tile + sizeof(Bars);
+    auto go = [&](auto kern, int tile, int tiles) {
+        const size_t smem = 1024 + (size_t)tiles * tile + sizeof(Bars);
         cudaError_t x = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (x != cudaSuccess) return x;
         kern<<<grid, NT, smem, st>>>(mq, mk, mv, mo, (__nv_bfloat16 *)O, a, tok, nblk, (int)items, starts);
         return cudaGetLastError();
     };
-    e = a.d == 64 ? go(window_fwd_kernel<64>, Cfg<64>::TILE, Cfg<64>::NST)
-                  : go(window_fwd_kernel<128>, Cfg<128>::TILE, Cfg<128>::NST);
+    e = a.d == 64 ? go(window_fwd_kernel<64>, Cfg<64>::TILE, 2 * Cfg<64>::QB + Cfg<64>::NST)
+                  : go(window_fwd_kernel<128>, Cfg<128>::TILE, 2 * Cfg<128>::QB + Cfg<128>::NST);
     if (e != cudaSuccess || !starts) return e;
-    const dim3 jg((unsigned)items, 2);
+    const dim3 jg((unsigned)items, 2 * JOIN_ROWS);
     if (a.d == 64) window_join_kernel<64><<<jg, 256, 0, st>>>(a, (__nv_bfloat16 *)O, tok, nblk, starts);
     else window_join_kernel<128><<<jg, 256, 0, st>>>(a, (__nv_bfloat16 *)O, tok, nblk, starts);
     return cudaGetLastError();
