@@ -486,9 +486,12 @@ HSA_API hsa_status_t hsa_paged_attend(const hsa_paged_t *p, const void *Q, const
 /*
  * Synchronises `stream`, then reads and clears the device-status word in the
  * workspace header.  Every call that takes a workspace clears that word when it
- * starts (stream-ordered), so the word describes the latest such call.
+ * starts (stream-ordered), so the word describes the latest such call; the
+ * local-attention calls only add to it, so there it describes all since it was
+ * last read.
  * Returns HSA_OK, HSA_ERR_TIMEOUT (a bounded device wait expired),
- * HSA_ERR_INVALID_ARG (hsa_attend skipped an out-of-range chunk index or keff)
+ * HSA_ERR_INVALID_ARG (hsa_attend skipped an out-of-range chunk index or keff, or
+ * a paged call a page number or length)
  * or HSA_ERR_CUDA (a CUDA call failed, or a kernel's own index check failed and
  * skipped the access, leaving that call's results incomplete).
  */

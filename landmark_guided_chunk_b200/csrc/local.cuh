@@ -59,8 +59,9 @@ __device__ __forceinline__ Seq seq_of(const LocArgs &a, int b) {
 // Row of the K/V tensors (in tokens) that holds token u of sequence b, or -1
 // if its page number is outside the pool.
 __device__ __forceinline__ long long kv_row(const LocArgs &a, int b, int u) {
-    if (!a.paged) return (long long)b * a.Tcap + u;
-    const int pg = a.table[(long long)b * a.max_pages + (u >> a.page_shift)];
+    if (!a.paged) return (long long)b * a.Tcap + dbg_clamp(u, 0, a.Tcap, a.status);
+    const int at = (int)dbg_clamp(u >> a.page_shift, 0, a.max_pages, a.status);
+    const int pg = a.table[(long long)b * a.max_pages + at];
     if ((unsigned)pg >= (unsigned)a.npages) {
         atomicOr(a.status, DEV_BAD_INDEX);
         return -1;

@@ -14,9 +14,13 @@
 //
 // Roles in both: four elementwise warpgroups (two take every other tile, each thread half of
 // a row's 64 columns), a loader warp (TMA), two or three MMA warps (converged, one lane
-// elected; a product that waits for its operands must not hold up the others), a helper warp.  Tiles are 128 x 64, so that S and dP fit TMEM twice next to the accumulators:
-// with one tile at a time, or with two warps per SM sub-partition, the elementwise latency
-// bounds the kernel (128 x 128 in 4300 and 3900 cycles; the products alone take 2500).
+// elected; a product that waits for its operands must not hold up the others), a helper
+// warp.  Tiles are 128 x 64, so that S and dP fit TMEM twice next to the accumulators.
+//
+// Bound: the hand-offs between product and elementwise warps, then the products.  16384
+// tokens, window 2048, 32 + 8 heads of 128: dK, dV 1.12 ms (its products alone 0.77, its
+// elementwise part alone 0.84), dQ 0.81 ms (0.55, 0.61); with tiles of 128 x 128 and two
+// elementwise warpgroups on the same tile 1.30 and 0.76.
 #include <stddef.h>
 
 #include "local.cuh"

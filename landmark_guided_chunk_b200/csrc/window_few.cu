@@ -10,6 +10,10 @@
 // CTAs' states are joined by O = sum 2^(m_i - m) O_i: within a cluster over
 // distributed shared memory (one launch, no workspace), or, for more splits than a
 // cluster holds, as partials that combine_kernel joins.
+//
+// 64 sequences of up to 16384 paged tokens, 32 + 8 heads of 128: 442 us, 5.7 TB/s (88% of
+// the measured copy rate); 8 sequences, window 4096: 27 us, 4.9 TB/s (256 CTAs on 148 SMs:
+// the SMs with two set the time).  The tcgen05 kernel, whose tiles hold 128 rows: 862 and 57 us.
 #include "decode_mma.cuh"
 #include "local.cuh"
 #include "sm100.cuh"

@@ -2,7 +2,13 @@
 // fp32 throughout: the fp32 problems' kernels, and the ones HSA_FLAG_SIMT asks
 // for.  Contiguous or paged K/V.  Also the pieces every path shares: the join
 // of key-axis splits, the row sums D of the backward, and the join of the
-// backward's far-sink partials.
+// backward's partials.
+//
+// 64 x 64 tiles, 4 x 4 elements a thread: each float4 read from shared memory
+// feeds 16 multiply-adds.  Bound: latency at small sizes (2 x 777 tokens, 4 heads
+// of 64, window 129: forward 33 us, dQ 47 us, about a quarter of the FMA rate on
+// 100 blocks), shared memory at large ones (bf16 inputs, 65536 tokens, window
+// 4096, 32 heads of 128: 28 TFLOP/s).
 #include "local.cuh"
 
 namespace hsa {

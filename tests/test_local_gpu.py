@@ -415,6 +415,43 @@ def test_paged_bad_pages_and_lengths():
     assert torch.equal(P.K, K0) and torch.equal(P.V, V0)
 
 
+def test_paged_shared_pages():
+    """A forked prefix: two sequences whose tables name the same pages, one of them twice in a row of the table."""
+    P = Pages(BF, 128, 8, 2, [1, 40, 1], [200, 200, 96], 32)
+    P.table[1, :5] = P.table[0, :5]
+    P.table[2, 1] = P.table[2, 0]
+    for kw in (dict(max_q=40, max_kv=200), dict(window=70, sinks=5)):
+        O = hsa.paged_attend(P.Q, P.K, P.V, P.q_start, P.kv_len, P.table, **kw)
+        for b in range(3):
+            r = Ref(P.Q[P.rows(b)], P.cache(b, P.K), P.cache(b, P.V), P.pos(b), P.kv[b], kw.get("window", 0), kw.get("sinks", 0))
+            check(f"O[{b}]", O[P.rows(b)], r.O, r.tO)
+
+
+def test_two_calls_at_once():
+    """The same inputs read by calls on two streams, each with its own workspace and outputs."""
+    T, W = 3000, 700
+    Q, K, V, dO = (_rand(i, BF, 1, T, h, 128) for i, h in enumerate((8, 2, 2, 8)))
+    O, lse = hsa.window_attend(Q, K, V, W, 4, return_lse=True)
+    want = (O,) + tuple(hsa.window_backward(Q, K, V, O, lse, dO, W, 4))
+    P = Pages(BF, 128, 8, 2, [300, 1], [9000, 9000], 64)
+    wantP = hsa.paged_attend(P.Q, P.K, P.V, P.q_start, P.kv_len, P.table, max_q=300, max_kv=9000)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i < 2:
+                    o, l = hsa.window_attend(Q, K, V, W, 4, return_lse=True)
+                    got.append((o,) + tuple(hsa.window_backward(Q, K, V, o, l, dO, W, 4)))
+                else:
+                    got.append((hsa.paged_attend(P.Q, P.K, P.V, P.q_start, P.kv_len, P.table, max_q=300, max_kv=9000),))
+    torch.cuda.synchronize()
+    for g in got:
+        w = want if len(g) > 1 else (wantP,)
+        assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("rot,inter,kw", [(64, False, dict()), (32, True, dict(scaling="linear", factor=2.0)),
                                           (20, False, dict(scaling="bands", factor=8.0, orig_len=64)), (0, False, dict())])
