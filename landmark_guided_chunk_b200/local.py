@@ -26,7 +26,9 @@ __all__ = ["make_rope", "rope", "window_workspace", "window_attend", "window_bac
 _DT = {torch.float32: _native.HSA_F32, torch.bfloat16: _native.HSA_BF16}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 _byref = ctypes.byref
-_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream(index).cuda_stream without the objects around it
+# torch.cuda.current_stream(index).cuda_stream and current_device() without the objects and checks around them
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _dtype(t):
@@ -58,10 +60,13 @@ def _check(like, *ts):
             raise TypeError(f"tensors of {dt} and {t.dtype}")
 
 
+_I32 = torch.int32
+
+
 def _ints(like, *names_tensors):
     dev = like.get_device()
     for name, t in names_tensors:
-        if t.dtype is not torch.int32:
+        if t.dtype is not _I32:
             raise TypeError(f"{name} must be int32, got {t.dtype}")
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and on {like.device}")
@@ -76,11 +81,16 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+_fns = {}   # the library's functions by name
+
+
 def _call(name, like, *args):
     """One library call on the current stream of `like`'s device, with that device current."""
-    fn = getattr(_native.lib(), name)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_native.lib(), name)
     index = like.get_device()
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
