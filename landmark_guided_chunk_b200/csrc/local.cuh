@@ -175,6 +175,7 @@ struct BwdPlan {
 };
 BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt);
 
+int simt_rows(const LocArgs &a);   // rows per block of the CUDA-core forward: 16, 32 or 64
 cudaError_t launch_simt(const LocArgs &a, int dtype, const void *Q, const void *K, const void *V, void *O,
                         cudaStream_t st);
 constexpr int FEW_CLUSTER = 8;   // splits that the few-row kernel joins within a cluster

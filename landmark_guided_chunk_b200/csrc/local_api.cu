@@ -158,7 +158,7 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
         if (n > 64) n = 64;
         if (n > 1) p.nsplit = (int)n;
     } else if (!p.tc) {
-        const int tok = 64 / a.G, bk = 64;
+        const int tok = simt_rows(a) / a.G, bk = 64;
         const long long items = (long long)ceil_div(a.max_q, tok) * a.Hkv * a.B;
         // too few blocks to fill the SMs twice: the key axis is split over CTAs as well, two tiles each at least
         const int nt = ceil_div(most_keys(a, tok), bk) + 1;

@@ -16,52 +16,57 @@ namespace local {
 
 namespace {
 
-constexpr int BM = 64;   // rows (token, head) per CTA
+constexpr int BM = 64;   // rows (token, head) per row tile of dK, dV
 constexpr int BN = 64;   // keys per tile
-constexpr int NT = 256;  // 16 x 16 threads: 4 rows x 4 keys of S each
+constexpr int NT = 256;  // 16 x 16 threads: RM rows x 4 keys of S each
 constexpr int PP = BN + 4;
 
-// Rows r0 .. r0+63 of a [rows][stride] tensor into shared memory as fp32 (pitch P);
-// row r is read at src(r), or zero where that is negative.
-template <typename T, int D, int P, typename Src>
+// R rows of a tensor into shared memory as fp32 (pitch P); row r is read at src(r), or
+// zero where that is negative.
+template <typename T, int D, int P, int R = 64, typename Src>
 __device__ __forceinline__ void load_rows(float *dst, const T *__restrict__ g, Src src) {
     constexpr int V = 16 / sizeof(T);    // elements per 16-byte load
     constexpr int PR = D / V;            // loads per row
-    for (int i = threadIdx.x; i < 64 * PR; i += NT) {
-        const int r = i / PR, c = (i % PR) * V;
-        const long long at = src(r);
-        float f[V];
-        if (at >= 0) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(g + at + c);
-            const T *t = reinterpret_cast<const T *>(&u);
+    constexpr int N = (R * PR + NT - 1) / NT;
+    uint4 u[N];
 #pragma unroll
-            for (int x = 0; x < V; ++x) f[x] = to_f32(t[x]);
-        } else {
-#pragma unroll
-            for (int x = 0; x < V; ++x) f[x] = 0.f;
+    for (int n = 0; n < N; ++n) {        // all of a thread's loads at once
+        const int i = threadIdx.x + n * NT;
+        u[n] = make_uint4(0, 0, 0, 0);
+        if (i < R * PR) {
+            const long long at = src(i / PR);
+            if (at >= 0) u[n] = *reinterpret_cast<const uint4 *>(g + at + i % PR * V);
         }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = threadIdx.x + n * NT;
+        if (i >= R * PR) continue;
+        const T *t = reinterpret_cast<const T *>(&u[n]);
+        float *d = dst + i / PR * P + i % PR * V;
 #pragma unroll
         for (int x = 0; x < V; x += 4)
-            *reinterpret_cast<float4 *>(dst + r * P + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+            *reinterpret_cast<float4 *>(d + x) =
+                make_float4(to_f32(t[x]), to_f32(t[x + 1]), to_f32(t[x + 2]), to_f32(t[x + 3]));
     }
 }
 
-// s[i][j] = row (ty*4 + i) of A . row (tx + 16 j) of B, over D
-template <int D, int PA, int PB>
-__device__ __forceinline__ void dot_tile(const float *A, const float *B, int ty, int tx, float (&s)[4][4]) {
+// s[i][j] = row (ty*RM + i) of A . row (tx + 16 j) of B, over D
+template <int D, int PA, int PB, int RM = 4>
+__device__ __forceinline__ void dot_tile(const float *A, const float *B, int ty, int tx, float (&s)[RM][4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RM; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
     for (int x = 0; x < D; x += 4) {
-        float4 a[4], b[4];
+        float4 a[RM], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (ty * 4 + i) * PA + x);
+        for (int i = 0; i < RM; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (ty * RM + i) * PA + x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * PB + x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RM; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
@@ -72,25 +77,25 @@ __device__ __forceinline__ void dot_tile(const float *A, const float *B, int ty,
     }
 }
 
-// acc[i][c] += sum_k P[row ty*4 + i][k] X[k][col], columns tx*4 + 64*(c/4) + c%4.
-// PT: P is stored [k][row] instead (transposed product).
-template <int D, int PX, bool PT>
-__device__ __forceinline__ void acc_tile(const float *Pm, const float *X, int ty, int tx, float (&acc)[4][D / 16]) {
+// acc[i][c] += sum_k P[row ty*RM + i][k] X[k][col], columns tx*4 + 64*(c/4) + c%4.
+// PT: P is stored [k][row] instead (transposed product; RM = 4).
+template <int D, int PX, bool PT, int RM = 4>
+__device__ __forceinline__ void acc_tile(const float *Pm, const float *X, int ty, int tx, float (&acc)[RM][D / 16]) {
 #pragma unroll 4
     for (int k = 0; k < 64; ++k) {
-        float p[4];
-        if (PT) {
+        float p[RM];
+        if constexpr (PT) {
             const float4 v = *reinterpret_cast<const float4 *>(Pm + k * PP + ty * 4);
             p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = Pm[(ty * 4 + i) * PP + k];
+            for (int i = 0; i < RM; ++i) p[i] = Pm[(ty * RM + i) * PP + k];
         }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
             const float4 v = *reinterpret_cast<const float4 *>(X + k * PX + tx * 4 + 64 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RM; ++i) {
                 acc[i][4 * c + 0] = fmaf(p[i], v.x, acc[i][4 * c + 0]);
                 acc[i][4 * c + 1] = fmaf(p[i], v.y, acc[i][4 * c + 1]);
                 acc[i][4 * c + 2] = fmaf(p[i], v.z, acc[i][4 * c + 2]);
@@ -125,10 +130,11 @@ __device__ __forceinline__ float sum16(float x) {
 
 // Forward: one pass over the block's key tiles with a running maximum m and
 // sum l per row; O is rescaled by exp(m_old - m_new) when the maximum grows.
-template <typename T, int D>
+template <typename T, int D, int RM>
 __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__restrict__ Q, const T *__restrict__ K,
                                                       const T *__restrict__ V, T *__restrict__ O) {
     extern __shared__ __align__(16) float sm[];
+    constexpr int BM = 16 * RM;   // rows (token, head) of this block
     float *sQ = sm, *sK = sQ + BM * D, *sV = sK + BN * (D + 4), *sP = sV + BN * D;
     const int b = blockIdx.z, j = blockIdx.y;
     const int split = blockIdx.x % a.nsplit, blk = blockIdx.x / a.nsplit;
@@ -141,15 +147,15 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
     int i0, i1;
     split_range(tl.nt, a.nsplit, split, &i0, &i1);
 
-    load_rows<T, D, D>(sQ, Q, [&](int r) -> long long {
+    load_rows<T, D, D, BM>(sQ, Q, [&](int r) -> long long {
         const int t = t0 + r / a.G;
         return r < tok * a.G && t < t1 ? ((long long)(s.row0 + t) * a.H + j * a.G + r % a.G) * D : -1;
     });
-    float m[4], l[4], o[4][D / 16];
-    int p[4];
+    float m[RM], l[RM], o[RM][D / 16];
+    int p[RM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
+    for (int i = 0; i < RM; ++i) {
+        const int r = ty * RM + i;
         m[i] = -INFINITY;
         l[i] = 0.f;
         p[i] = r < tok * a.G && t0 + r / a.G < t1 ? s.pos0 + t0 + r / a.G : -1;   // -1: sees nothing
@@ -167,10 +173,10 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
         load_rows<T, D, D + 4>(sK, K, src);
         load_rows<T, D, D>(sV, V, src);
         __syncthreads();
-        float sc[4][4];
-        dot_tile<D, D, D + 4>(sQ, sK, ty, tx, sc);
+        float sc[RM][4];
+        dot_tile<D, D, D + 4, RM>(sQ, sK, ty, tx, sc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RM; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
             for (int c = 0; c < 4; ++c) {
                 const float e = exp2f(sc[i][c] - ref);
                 sum += e;
-                sP[(ty * 4 + i) * PP + tx + 16 * c] = e;
+                sP[(ty * RM + i) * PP + tx + 16 * c] = e;
             }
             l[i] = l[i] * f + sum16(sum);
             m[i] = mx;
@@ -194,11 +200,11 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
         __syncwarp();   // a warp reads only the P rows that it wrote
-        acc_tile<D, D, false>(sP, sV, ty, tx, o);
+        acc_tile<D, D, false, RM>(sP, sV, ty, tx, o);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
+    for (int i = 0; i < RM; ++i) {
+        const int r = ty * RM + i;
         if (r >= tok * a.G || t0 + r / a.G >= t1) continue;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         const float lse = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
@@ -288,12 +294,13 @@ __global__ void __launch_bounds__(256) rowdot_kernel(const T *__restrict__ O, co
 }
 
 // dQ: the forward's iteration; P from lse, dP = dO V^T, dS = P (dP - D), dQ += dS K.
-template <typename T, int D>
+template <typename T, int D, int RM>
 __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restrict__ Q, const T *__restrict__ K,
                                                      const T *__restrict__ V, const T *__restrict__ dO,
                                                      T *__restrict__ dQ) {
     extern __shared__ __align__(16) float sm[];
     const LocArgs &a = w.a;
+    constexpr int BM = 16 * RM;
     float *sQ = sm, *sG = sQ + BM * D, *sK = sG + BM * D, *sV = sK + BN * (D + 4), *sP = sV + BN * (D + 4);
     const int b = blockIdx.z, j = blockIdx.y;
     const int tok = BM / a.G;
@@ -305,14 +312,14 @@ __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restr
         const int t = t0 + r / a.G;
         return r < tok * a.G && t < t1 ? ((long long)(s.row0 + t) * a.H + j * a.G + r % a.G) * D : -1;
     };
-    load_rows<T, D, D>(sQ, Q, qsrc);
-    load_rows<T, D, D>(sG, dO, qsrc);
-    float lse2[4], dd[4], acc[4][D / 16];
-    int p[4];
+    load_rows<T, D, D, BM>(sQ, Q, qsrc);
+    load_rows<T, D, D, BM>(sG, dO, qsrc);
+    float lse2[RM], dd[RM], acc[RM][D / 16];
+    int p[RM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long at = qsrc(ty * 4 + i);
-        p[i] = at >= 0 ? s.pos0 + t0 + (ty * 4 + i) / a.G : -1;
+    for (int i = 0; i < RM; ++i) {
+        const long long at = qsrc(ty * RM + i);
+        p[i] = at >= 0 ? s.pos0 + t0 + (ty * RM + i) / a.G : -1;
         lse2[i] = at >= 0 ? a.lse[at / D] * 1.4426950408889634f : 0.f;
         dd[i] = at >= 0 ? w.D[at / D] : 0.f;
 #pragma unroll
@@ -327,23 +334,23 @@ __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restr
         load_rows<T, D, D + 4>(sK, K, src);
         load_rows<T, D, D + 4>(sV, V, src);
         __syncthreads();
-        float sc[4][4], dp[4][4];
-        dot_tile<D, D, D + 4>(sQ, sK, ty, tx, sc);
-        dot_tile<D, D, D + 4>(sG, sV, ty, tx, dp);
+        float sc[RM][4], dp[RM][4];
+        dot_tile<D, D, D + 4, RM>(sQ, sK, ty, tx, sc);
+        dot_tile<D, D, D + 4, RM>(sG, sV, ty, tx, dp);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RM; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const bool vis = visible(p[i], u0 + tx + 16 * c, s.kv, a.window, a.sinks);
                 const float pr = vis ? exp2f(fmaf(sc[i][c], a.scale_log2, -lse2[i])) : 0.f;
-                sP[(ty * 4 + i) * PP + tx + 16 * c] = vis ? pr * (dp[i][c] - dd[i]) : 0.f;
+                sP[(ty * RM + i) * PP + tx + 16 * c] = vis ? pr * (dp[i][c] - dd[i]) : 0.f;
             }
         __syncwarp();
-        acc_tile<D, D + 4, false>(sP, sK, ty, tx, acc);
+        acc_tile<D, D + 4, false, RM>(sP, sK, ty, tx, acc);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long at = qsrc(ty * 4 + i);
+    for (int i = 0; i < RM; ++i) {
+        const long long at = qsrc(ty * RM + i);
         if (at < 0) continue;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
@@ -471,31 +478,49 @@ template <typename F> cudaError_t with_smem(F f, size_t bytes) {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int D>
-cudaError_t fwd(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
+template <typename T, int D, int RM>
+cudaError_t fwd_rows(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
+    constexpr int BM = 16 * RM;
     const size_t smem = (BM * D + BN * (D + 4) + BN * D + BM * PP) * sizeof(float);
-    cudaError_t e = with_smem(simt_fwd_kernel<T, D>, smem);
+    cudaError_t e = with_smem(simt_fwd_kernel<T, D, RM>, smem);
     if (e != cudaSuccess) return e;
     const int tok = BM / a.G;
     const dim3 grid((unsigned)((a.max_q + tok - 1) / tok) * a.nsplit, a.Hkv, a.B);
-    simt_fwd_kernel<T, D><<<grid, NT, smem, st>>>(a, (const T *)Q, (const T *)K, (const T *)V, (T *)O);
+    simt_fwd_kernel<T, D, RM><<<grid, NT, smem, st>>>(a, (const T *)Q, (const T *)K, (const T *)V, (T *)O);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t fwd(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
+    const int rows = simt_rows(a);
+    return rows == 16   ? fwd_rows<T, D, 1>(a, Q, K, V, O, st)
+           : rows == 32 ? fwd_rows<T, D, 2>(a, Q, K, V, O, st)
+                        : fwd_rows<T, D, 4>(a, Q, K, V, O, st);
+}
+
+template <typename T, int D, int RM>
+cudaError_t dq_rows(const BwdArgs &w, const void *Q, const void *K, const void *V, const void *dO, void *dQ,
+                    cudaStream_t st) {
+    constexpr int BM = 16 * RM;
+    const size_t smem = (2 * BM * D + 2 * BN * (D + 4) + BM * PP) * sizeof(float);
+    cudaError_t e = with_smem(simt_dq_kernel<T, D, RM>, smem);
+    if (e != cudaSuccess) return e;
+    const int tok = BM / w.a.G;
+    simt_dq_kernel<T, D, RM><<<dim3((w.a.max_q + tok - 1) / tok, w.a.Hkv, w.a.B), NT, smem, st>>>(
+        w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dQ);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t bwd(const BwdArgs &w, const void *Q, const void *K, const void *V, const void *dO, void *dQ, void *dK,
                 void *dV, cudaStream_t st) {
-    const size_t s1 = (2 * BM * D + 2 * BN * (D + 4) + BM * PP) * sizeof(float);
-    const size_t s2 = (4 * BN * (D + 4) + 2 * BM * PP) * sizeof(float);
-    cudaError_t e = with_smem(simt_dq_kernel<T, D>, s1);
-    if (e == cudaSuccess) e = with_smem(simt_dkv_kernel<T, D>, s2);
+    const size_t smem = (4 * BN * (D + 4) + 2 * BM * PP) * sizeof(float);
+    cudaError_t e = with_smem(simt_dkv_kernel<T, D>, smem);
+    if (e == cudaSuccess && w.a.max_q > 0)
+        e = simt_rows(w.a) < 64 ? dq_rows<T, D, 2>(w, Q, K, V, dO, dQ, st) : dq_rows<T, D, 4>(w, Q, K, V, dO, dQ, st);
     if (e != cudaSuccess) return e;
-    const int tok = BM / w.a.G;
-    if (w.a.max_q > 0)
-        simt_dq_kernel<T, D><<<dim3((w.a.max_q + tok - 1) / tok, w.a.Hkv, w.a.B), NT, s1, st>>>(
-            w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dQ);
     if (w.nkt > 0)
-        simt_dkv_kernel<T, D><<<dim3(w.nkt * w.nwin + w.nst * w.nfar, w.a.Hkv, w.a.B), NT, s2, st>>>(
+        simt_dkv_kernel<T, D><<<dim3(w.nkt * w.nwin + w.nst * w.nfar, w.a.Hkv, w.a.B), NT, smem, st>>>(
             w, (const T *)Q, (const T *)K, (const T *)V, (const T *)dO, (T *)dK, (T *)dV);
     return cudaGetLastError();
 }
@@ -504,6 +529,14 @@ cudaError_t bwd(const BwdArgs &w, const void *Q, const void *K, const void *V, c
     (dtype == HSA_F32 ? (d == 64 ? call_f64 : call_f128) : (d == 64 ? call_b64 : call_b128))
 
 }  // namespace
+
+int simt_rows(const LocArgs &a) {
+    // few rows in all: 16; few blocks: 32, so that more SMs and more warps per SM have some (2 x 777 tokens of 4
+    // heads, window 129: SIMTROWS); else 64, which reads the keys half as often
+    if ((long long)a.max_q * a.G <= 16) return 16;
+    const int tok = 64 / a.G;
+    return (long long)((a.max_q + tok - 1) / tok) * a.Hkv * a.B < 2 * 148 ? 32 : 64;
+}
 
 cudaError_t launch_simt(const LocArgs &a, int dtype, const void *Q, const void *K, const void *V, void *O,
                         cudaStream_t st) {
