@@ -60,6 +60,10 @@ struct PollLimit {
     }
 };
 
+// Bound of a wait that lasts a whole work item (a row block over all its keys), not a tile: 16M keys take a quarter
+// of a second.
+constexpr uint64_t ITEM_WAIT_NS = 30000000000ull;
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(NTQ, 1)
                     }
                     ++nk;
                     if (i == 0) {
-                        if (nq > 0 && !(ok = mbar_wait(&bar->q_empty, (nq - 1) & 1, abort, status))) break;
+                        if (nq > 0 && !(ok = mbar_wait(&bar->q_empty, (nq - 1) & 1, abort, status, ITEM_WAIT_NS))) break;
                         ++nq;
                         if (lane == 0) {
                             mbar_expect_tx(&bar->q_full, 2 * qbytes);
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(NTK, 1)
             for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
                 const KvItem it = kv_item(w, idx, tok);
                 if (it.nt == 0) continue;
-                if (ni > 0 && !(ok = mbar_wait(&bar->kv_empty, (ni - 1) & 1, abort, status))) break;
+                if (ni > 0 && !(ok = mbar_wait(&bar->kv_empty, (ni - 1) & 1, abort, status, ITEM_WAIT_NS))) break;
                 ++ni;
                 if (lane == 0) {
                     mbar_expect_tx(&bar->kv_full, 2 * C::TILE);

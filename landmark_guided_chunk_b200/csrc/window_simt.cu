@@ -4,12 +4,13 @@
 // of key-axis splits, the row sums D of the backward, and the join of the
 // backward's partials.
 //
-// 64 x 64 tiles, 4 x 4 elements a thread: each float4 read from shared memory
-// feeds 16 multiply-adds.  Bound: latency at small sizes (2 x 777 tokens, 4 heads
-// of 64, window 129: forward 33 us, dQ 47 us, about a quarter of the FMA rate on
-// 100 blocks), shared memory at large ones (bf16 inputs, 65536 tokens, window
-// 4096, 32 heads of 128: 28 TFLOP/s).
+// 64 x 64 tiles, 4 x 4 elements a thread (16 or 32 rows where there are few).  Bound:
+// latency at small sizes (2 x 777 tokens, 4 heads of 64, window 129: forward 34 us, dQ
+// 42 us, dK and dV 59 us on 100 to 200 blocks of two warps per SM sub-partition, which
+// wait for shared memory), shared memory at large ones (bf16 inputs, 65536 tokens,
+// window 4096, 32 heads of 128: 28 TFLOP/s).
 #include "local.cuh"
+#include "local_sm100.cuh"
 
 namespace hsa {
 namespace local {
@@ -51,37 +52,44 @@ __device__ __forceinline__ void load_rows(float *dst, const T *__restrict__ g, S
     }
 }
 
-// s[i][j] = row (ty*RM + i) of A . row (tx + 16 j) of B, over D
+// Packed fp32 pairs (one instruction does two multiply-adds): these loops are bound by issue.
+__device__ __forceinline__ ulonglong2 ld_pairs(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
+
+// s[i][j] = row (ty*RM + i) of A . row (tx + 16 j) of B, over D; even and odd elements are summed apart
 template <int D, int PA, int PB, int RM = 4>
 __device__ __forceinline__ void dot_tile(const float *A, const float *B, int ty, int tx, float (&s)[RM][4]) {
+    uint64_t t[RM][4];
 #pragma unroll
     for (int i = 0; i < RM; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+        for (int j = 0; j < 4; ++j) t[i][j] = 0;
+#pragma unroll 8
     for (int x = 0; x < D; x += 4) {
-        float4 a[RM], b[4];
+        ulonglong2 a[RM], b[4];
 #pragma unroll
-        for (int i = 0; i < RM; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (ty * RM + i) * PA + x);
+        for (int i = 0; i < RM; ++i) a[i] = ld_pairs(A + (ty * RM + i) * PA + x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * PB + x);
+        for (int j = 0; j < 4; ++j) b[j] = ld_pairs(B + (tx + 16 * j) * PB + x);
 #pragma unroll
         for (int i = 0; i < RM; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
-            }
+            for (int j = 0; j < 4; ++j) t[i][j] = sm100::fma2(a[i].y, b[j].y, sm100::fma2(a[i].x, b[j].x, t[i][j]));
     }
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            sm100::unpair(t[i][j], lo, hi);
+            s[i][j] = lo + hi;
+        }
 }
 
-// acc[i][c] += sum_k P[row ty*RM + i][k] X[k][col], columns tx*4 + 64*(c/4) + c%4.
+// acc[i][c] += sum_k P[row ty*RM + i][k] X[k][col]; acc's pair c: columns tx*4 + 64*(c/2) + 2*(c%2), and the next.
 // PT: P is stored [k][row] instead (transposed product; RM = 4).
 template <int D, int PX, bool PT, int RM = 4>
-__device__ __forceinline__ void acc_tile(const float *Pm, const float *X, int ty, int tx, float (&acc)[RM][D / 16]) {
-#pragma unroll 4
+__device__ __forceinline__ void acc_tile(const float *Pm, const float *X, int ty, int tx, uint64_t (&acc)[RM][D / 32]) {
+#pragma unroll 8
     for (int k = 0; k < 64; ++k) {
         float p[RM];
         if constexpr (PT) {
@@ -91,15 +99,16 @@ __device__ __forceinline__ void acc_tile(const float *Pm, const float *X, int ty
 #pragma unroll
             for (int i = 0; i < RM; ++i) p[i] = Pm[(ty * RM + i) * PP + k];
         }
+        uint64_t pp[RM];
+#pragma unroll
+        for (int i = 0; i < RM; ++i) pp[i] = sm100::pair(p[i], p[i]);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            const float4 v = *reinterpret_cast<const float4 *>(X + k * PX + tx * 4 + 64 * c);
+            const ulonglong2 v = ld_pairs(X + k * PX + tx * 4 + 64 * c);
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
-                acc[i][4 * c + 0] = fmaf(p[i], v.x, acc[i][4 * c + 0]);
-                acc[i][4 * c + 1] = fmaf(p[i], v.y, acc[i][4 * c + 1]);
-                acc[i][4 * c + 2] = fmaf(p[i], v.z, acc[i][4 * c + 2]);
-                acc[i][4 * c + 3] = fmaf(p[i], v.w, acc[i][4 * c + 3]);
+                acc[i][2 * c] = sm100::fma2(pp[i], v.x, acc[i][2 * c]);
+                acc[i][2 * c + 1] = sm100::fma2(pp[i], v.y, acc[i][2 * c + 1]);
             }
         }
     }
@@ -151,7 +160,8 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
         const int t = t0 + r / a.G;
         return r < tok * a.G && t < t1 ? ((long long)(s.row0 + t) * a.H + j * a.G + r % a.G) * D : -1;
     });
-    float m[RM], l[RM], o[RM][D / 16];
+    float m[RM], l[RM];
+    uint64_t o[RM][D / 32];   // pairs of columns
     int p[RM];
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
@@ -160,7 +170,7 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
         l[i] = 0.f;
         p[i] = r < tok * a.G && t0 + r / a.G < t1 ? s.pos0 + t0 + r / a.G : -1;   // -1: sees nothing
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) o[i][c] = 0;
     }
     for (int it = i0; it < i1; ++it) {
         const int u0 = tl.tile(it) * BN;
@@ -197,7 +207,7 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
             l[i] = l[i] * f + sum16(sum);
             m[i] = mx;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
+            for (int c = 0; c < D / 32; ++c) o[i][c] = sm100::fma2(o[i][c], sm100::pair(f, f), 0);
         }
         __syncwarp();   // a warp reads only the P rows that it wrote
         acc_tile<D, D, false, RM>(sP, sV, ty, tx, o);
@@ -212,8 +222,10 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
         const long long prow = (long long)split * a.rows * a.H + row;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            const float x = o[i][4 * c] * inv, y = o[i][4 * c + 1] * inv, z = o[i][4 * c + 2] * inv,
-                        w = o[i][4 * c + 3] * inv;
+            float x, y, z, w;
+            sm100::unpair(o[i][2 * c], x, y);
+            sm100::unpair(o[i][2 * c + 1], z, w);
+            x *= inv, y *= inv, z *= inv, w *= inv;
             if (a.nsplit > 1)
                 store4<float>(a.opart + prow * D + tx * 4 + 64 * c, x, y, z, w);
             else
@@ -314,7 +326,8 @@ __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restr
     };
     load_rows<T, D, D, BM>(sQ, Q, qsrc);
     load_rows<T, D, D, BM>(sG, dO, qsrc);
-    float lse2[RM], dd[RM], acc[RM][D / 16];
+    float lse2[RM], dd[RM];
+    uint64_t acc[RM][D / 32];
     int p[RM];
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restr
         lse2[i] = at >= 0 ? a.lse[at / D] * 1.4426950408889634f : 0.f;
         dd[i] = at >= 0 ? w.D[at / D] : 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = 0;
     }
     for (int it = 0; it < tl.nt; ++it) {
         const int u0 = tl.tile(it) * BN;
@@ -353,9 +366,12 @@ __global__ void __launch_bounds__(NT) simt_dq_kernel(BwdArgs w, const T *__restr
         const long long at = qsrc(ty * RM + i);
         if (at < 0) continue;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-            store4<T>(dQ + at + tx * 4 + 64 * c, acc[i][4 * c] * a.scale, acc[i][4 * c + 1] * a.scale,
-                      acc[i][4 * c + 2] * a.scale, acc[i][4 * c + 3] * a.scale);
+        for (int c = 0; c < D / 64; ++c) {
+            float x, y, z, v;
+            sm100::unpair(acc[i][2 * c], x, y);
+            sm100::unpair(acc[i][2 * c + 1], z, v);
+            store4<T>(dQ + at + tx * 4 + 64 * c, x * a.scale, y * a.scale, z * a.scale, v * a.scale);
+        }
     }
 }
 
@@ -379,11 +395,11 @@ __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__rest
         return u0 + r < s.kv ? (kv_row(a, b, u0 + r) * a.Hkv + j) * D : -1;
     };
     const int tok = BM / a.G;
-    float gk[4][D / 16], gv[4][D / 16];
+    uint64_t gk[4][D / 32], gv[4][D / 32];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) gk[i][c] = gv[i][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) gk[i][c] = gv[i][c] = 0;
     if (ta < tb) {
         load_rows<T, D, D + 4>(sK, K, src);
         load_rows<T, D, D + 4>(sV, V, src);
@@ -431,9 +447,11 @@ __global__ void __launch_bounds__(NT) simt_dkv_kernel(BwdArgs w, const T *__rest
             const int col = tx * 4 + 64 * c;
             float k4[4], v4[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                k4[x] = gk[i][4 * c + x] * a.scale;
-                v4[x] = gv[i][4 * c + x];
+            for (int x = 0; x < 4; x += 2) {
+                sm100::unpair(gk[i][2 * c + x / 2], k4[x], k4[x + 1]);
+                sm100::unpair(gv[i][2 * c + x / 2], v4[x], v4[x + 1]);
+                k4[x] *= a.scale;
+                k4[x + 1] *= a.scale;
             }
             if (part) {
                 const long long at = (((long long)b * a.Hkv + j) * w.npt * BN + u) * D + col;
@@ -532,7 +550,8 @@ cudaError_t bwd(const BwdArgs &w, const void *Q, const void *K, const void *V, c
 
 int simt_rows(const LocArgs &a) {
     // few rows in all: 16; few blocks: 32, so that more SMs and more warps per SM have some (2 x 777 tokens of 4
-    // heads, window 129: SIMTROWS); else 64, which reads the keys half as often
+    // heads, window 129: 34 us; 40 with 64 rows and the
+    // keys in two splits); else 64, which reads the keys half as often
     if ((long long)a.max_q * a.G <= 16) return 16;
     const int tok = 64 / a.G;
     return (long long)((a.max_q + tok - 1) / tok) * a.Hkv * a.B < 2 * 148 ? 32 : 64;

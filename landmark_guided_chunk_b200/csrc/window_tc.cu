@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(NT, 1)
                             for (int t = 0; t < it.ntile && ok; ++t) {
                                 const uint32_t bit = 1u << (2 * x + t);
                                 if ((qused & bit) &&
-                                    !(ok = mbar_wait(&bar->q_empty[x][t], (qpar & bit) ? 0 : 1, abort, status)))
+                                    !(ok = mbar_wait(&bar->q_empty[x][t], (qpar & bit) ? 0 : 1, abort, status, ITEM_WAIT_NS)))
                                     break;
                                 qused |= bit;
                                 qpar ^= bit;
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 const int x = na++ % C::QB;
                 for (int t = 0; t < it.ntile; ++t) {
-                    if (!(ok = mbar_wait(&bar->out_full[t], par >> t & 1, abort, status))) break;
+                    if (!(ok = mbar_wait(&bar->out_full[t], par >> t & 1, abort, status, ITEM_WAIT_NS))) break;
                     par ^= 1u << t;
                     if (lane == 0) {
                         if (it.slot < 0 && it.t0 + (t + 1) * tok <= it.s.n) {
