@@ -387,11 +387,12 @@ HSA_API hsa_status_t hsa_window_attend(const hsa_window_t *p, const void *Q, con
 
 /*
  * Gradients of hsa_window_attend with respect to Q, K and V for the upstream dO:
- *   D = sum(dO o O);  P = exp(scale q . k - lse);  dS = P o (dO . v - D)
+ *   P = exp(scale q . k - lse);  D = sum(dO o O);  dS = P o (dO . v - D)
  *   dV = sum P dO,  dQ = scale sum dS k,  dK = scale sum dS q   (dK, dV over all G heads of the group)
  * in the problem's dtype, rounded once from fp32 sums and OVERWRITTEN: dQ [B][Tq][H][d], dK and dV
  * [B][Tcap][Hkv][d] (zeros for tokens that no query sees).  O and lse as hsa_window_attend returned
- * them.  bf16 rounds P and dS to bf16 before their products.  No atomics: equal calls give equal bits.
+ * them.  bf16 rounds P and dS to bf16 before their products; where a row sees few keys (up to 64), D is
+ * sum P (dO . v) in fp32, without the rounding of the bf16 O.  No atomics: equal calls give equal bits.
  */
 HSA_API hsa_status_t hsa_window_backward_workspace_size(const hsa_window_t *p, size_t *bytes);
 HSA_API hsa_status_t hsa_window_backward(const hsa_window_t *p, const void *Q, const void *K, const void *V,

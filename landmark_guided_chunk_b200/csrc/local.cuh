@@ -126,7 +126,7 @@ struct BwdArgs {
     int nst;                         // key tiles that hold sinks and have a far part (0: none)
     int nfar, far_q;
     int npt;                         // key tiles written as partials: the first npt
-    float *D;                        // [B][Tq][H] row sums of dO o O
+    float *D;                        // [B][Tq][H] row sums of dO o O (few keys: of P o dP)
     float *part;                     // [2 (dK, dV)][nwin + nfar][B][Hkv][npt * BK][d]
 };
 
@@ -190,6 +190,10 @@ TcPlan tc_plan(const LocArgs &a, long long most_keys);   // most_keys: that one 
 cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st);
 cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st);
+// bf16: D of the rows that see few keys
+bool few_rowdot_all(const LocArgs &a);   // that is every row
+cudaError_t launch_few_rowdot(const LocArgs &a, const void *Q, const void *K, const void *V, const void *dO, float *D,
+                              cudaStream_t st);
 cudaError_t launch_bwd_simt(const BwdArgs &w, int dtype, const void *Q, const void *K, const void *V, const void *dO,
                             void *dQ, void *dK, void *dV, cudaStream_t st);
 bool bwd_tc_supported(const LocArgs &a, int dtype);

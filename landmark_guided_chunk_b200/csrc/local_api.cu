@@ -312,7 +312,9 @@ hsa_status_t hsa_window_backward(const hsa_window_t *prob, const void *Q, const 
         if (e == cudaSuccess) e = cudaMemset2DAsync((char *)dV + tail * row, pitch, 0, row * (a.Tcap - tail), a.B, st);
     }
     if (e == cudaSuccess && rows) {
-        e = launch_rowdot(a, prob->dtype, O, dO, w.D, st);
+        const bool few = prob->dtype == HSA_BF16;
+        if (!few || !few_rowdot_all(a)) e = launch_rowdot(a, prob->dtype, O, dO, w.D, st);
+        if (e == cudaSuccess && few) e = launch_few_rowdot(a, Q, K, V, dO, w.D, st);
         if (e == cudaSuccess)
             e = pl.tc ? launch_bwd_tc(w, Q, K, V, dO, dQ, dK, dV, st)
                       : launch_bwd_simt(w, prob->dtype, Q, K, V, dO, dQ, dK, dV, st);

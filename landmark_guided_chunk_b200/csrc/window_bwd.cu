@@ -1,6 +1,7 @@
 // window_bwd.cu -- backward of the sliding-window attention on tcgen05 (bf16).
 //
-// With P = exp2(scale_log2 S - lse_log2), S = Q K^T, dP = dO V^T, D = rowsum(dO o O):
+// With P = exp2(scale_log2 S - lse_log2), S = Q K^T, dP = dO V^T, D = rowsum(dO o O)
+// (few keys: rowsum(P o dP), few_rowdot_kernel):
 //   dS = P o (dP - D),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
 // Two kernels, each writing its outputs once, so that no sum depends on the order of
 // atomics: window_dq_kernel runs over the key tiles of a row tile (three products per

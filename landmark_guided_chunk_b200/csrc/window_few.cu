@@ -356,6 +356,92 @@ __global__ void __launch_bounds__(NT) window_few_kernel(const __grid_constant__ 
     if constexpr (CLUSTER) cluster_sync();   // peers may still read this CTA's shared memory
 }
 
+// D of the query rows that see few keys, for the backward: D = sum_u P[u] dP[u], P = exp(scale S - lse), dP = dO . V[u],
+// in fp32.  dO . O is the same in exact arithmetic, but the bf16 O is off by 2^-9 of itself, and over n equal keys that
+// part of dQ and dK is about 1 / sqrt(n) of the one that rounding dS leaves: as large with one key, nothing with many.
+// A warp takes 16 rows (token, head of the group), keys in eights; 16-byte chunks go straight to the fragments (the
+// contraction runs over the elements in any order that both operands share).
+//
+// DOT_KEYS: the gradients' error against 64 bits with 64 keys or fewer was up to 1.6 times that of rounding the exact
+// result once, and is 1.4 times with this kernel (rounding dS and the result).  2 x 4096 tokens, 32 + 8 heads of 128:
+// the whole backward takes 232 us with a window of 64, 199 with one of 65 (which leaves the kernel 64 tokens), 182
+// with 16.
+constexpr int DOT_KEYS = 64;
+
+__device__ __forceinline__ int keys_seen(const LocArgs &a, int p) {
+    const int hi = min(p + 1, a.max_kv), lo = min(p >= a.window ? p - a.window + 1 : 0, hi);
+    return hi - lo + min(a.sinks, lo);
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) few_rowdot_kernel(LocArgs a, const __nv_bfloat16 *__restrict__ Q,
+                                                         const __nv_bfloat16 *__restrict__ K,
+                                                         const __nv_bfloat16 *__restrict__ V,
+                                                         const __nv_bfloat16 *__restrict__ dO, float *__restrict__ out,
+                                                         int ntok) {
+    constexpr int C = D / 32;   // 16-byte chunks of a row per lane
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, j = blockIdx.y, b = blockIdx.z;
+    const long long n = (long long)ntok * a.G, e0 = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * 16;
+    if (e0 >= n) return;
+    int pos[2];
+    long long row[2];
+    float nl[2];
+    uint4 q[2][C], d[2][C];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const long long e = min(e0 + g + 8 * x, n - 1);   // rows behind the last repeat it
+        const int t = (int)(e / a.G);
+        pos[x] = a.q_pos0 + t;
+        row[x] = ((long long)b * a.max_q + t) * a.H + j * a.G + (int)(e % a.G);
+    }
+    if (!__any_sync(FULL, min(keys_seen(a, pos[0]), keys_seen(a, pos[1])) <= DOT_KEYS)) return;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        nl[x] = a.lse[row[x]] * -1.4426950408889634f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            q[x][i] = reinterpret_cast<const uint4 *>(Q + row[x] * D)[c + 4 * i];
+            d[x][i] = reinterpret_cast<const uint4 *>(dO + row[x] * D)[c + 4 * i];
+        }
+    }
+    const int pa = a.q_pos0 + (int)(e0 / a.G), pb = a.q_pos0 + (int)(min(e0 + 15, n - 1) / a.G);
+    const int hi = min(pb + 1, a.max_kv), lo = min(pa >= a.window ? pa - a.window + 1 : 0, hi);
+    float sum[2] = {0.f, 0.f};
+    for (int part = 0; part < 2; ++part) {   // sinks before the window, then the window
+        const int ua = part ? lo : 0, ub = part ? hi : min(a.sinks, lo);
+        for (int u0 = ua; u0 < ub; u0 += 8) {
+            const long long at = ((kv_row(a, b, min(u0 + g, ub - 1))) * a.Hkv + j) * D;
+            uint4 k[C], v[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                k[i] = reinterpret_cast<const uint4 *>(K + at)[c + 4 * i];
+                v[i] = reinterpret_cast<const uint4 *>(V + at)[c + 4 * i];
+            }
+            float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                mma16816(s, q[0][i].x, q[1][i].x, q[0][i].y, q[1][i].y, k[i].x, k[i].y);
+                mma16816(dp, d[0][i].x, d[1][i].x, d[0][i].y, d[1][i].y, v[i].x, v[i].y);
+                mma16816(s, q[0][i].z, q[1][i].z, q[0][i].w, q[1][i].w, k[i].z, k[i].w);
+                mma16816(dp, d[0][i].z, d[1][i].z, d[0][i].w, d[1][i].w, v[i].z, v[i].w);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int x = y >> 1, u = u0 + 2 * c + (y & 1);
+                const float pr = exp2f(fmaf(s[y], a.scale_log2, nl[x])) * dp[y];
+                // selected, not multiplied: keys that a row does not see may hold NaN
+                sum[x] += u < ub && visible(pos[x], u, a.max_kv, a.window, a.sinks) ? pr : 0.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        sum[x] += __shfl_xor_sync(FULL, sum[x], 1);
+        sum[x] += __shfl_xor_sync(FULL, sum[x], 2);
+        if (c == 0 && e0 + g + 8 * x < n) out[row[x]] = sum[x];
+    }
+}
+
 }  // namespace
 
 bool few_supported(const LocArgs &a, int dtype) {
@@ -394,6 +480,25 @@ cudaError_t launch_few(const LocArgs &a, const void *Q, const void *K, const voi
                        : go(window_few_kernel<64, false>, Shape<64>::STAGE, false);
     return cluster ? go(window_few_kernel<128, true>, Shape<128>::STAGE, true)
                    : go(window_few_kernel<128, false>, Shape<128>::STAGE, false);
+}
+
+bool few_rowdot_all(const LocArgs &a) {
+    return a.max_kv > 0 && a.window <= DOT_KEYS && a.sinks <= DOT_KEYS - a.window;
+}
+
+cudaError_t launch_few_rowdot(const LocArgs &a, const void *Q, const void *K, const void *V, const void *dO, float *D,
+                              cudaStream_t st) {
+    // all tokens with a window of few keys, or where queries run past the keys; else the first ones
+    const bool all = a.window <= DOT_KEYS || (long long)a.q_pos0 + a.max_q > a.max_kv;
+    const int ntok = all ? a.max_q : max(0, min(a.max_q, DOT_KEYS - a.q_pos0));
+    if (ntok == 0 || a.max_kv == 0) return cudaSuccess;
+    typedef __nv_bfloat16 h;
+    const dim3 grid((unsigned)(((long long)ntok * a.G + 63) / 64), a.Hkv, a.B);
+    if (a.d == 64)
+        few_rowdot_kernel<64><<<grid, 128, 0, st>>>(a, (const h *)Q, (const h *)K, (const h *)V, (const h *)dO, D, ntok);
+    else
+        few_rowdot_kernel<128><<<grid, 128, 0, st>>>(a, (const h *)Q, (const h *)K, (const h *)V, (const h *)dO, D, ntok);
+    return cudaGetLastError();
 }
 
 }  // namespace local

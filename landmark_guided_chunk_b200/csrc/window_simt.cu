@@ -550,8 +550,7 @@ cudaError_t bwd(const BwdArgs &w, const void *Q, const void *K, const void *V, c
 
 int simt_rows(const LocArgs &a) {
     // few rows in all: 16; few blocks: 32, so that more SMs and more warps per SM have some (2 x 777 tokens of 4
-    // heads, window 129: 34 us; 40 with 64 rows and the
-    // keys in two splits); else 64, which reads the keys half as often
+    // heads, window 129: 34 us; 40 with 64 rows and the keys in two splits); else 64, which reads the keys half as often
     if ((long long)a.max_q * a.G <= 16) return 16;
     const int tok = 64 / a.G;
     return (long long)((a.max_q + tok - 1) / tok) * a.Hkv * a.B < 2 * 148 ? 32 : 64;

@@ -38,7 +38,7 @@ def seen(p, n_keys, kv, window, sinks):
 class Ref:
     """One sequence: Q [n,H,d], K, V [m,Hkv,d] as stored; p [n] positions; kv cached tokens (<= m)."""
 
-    def __init__(self, Q, K, V, p, kv, window, sinks, scale=None, dO=None):
+    def __init__(self, Q, K, V, p, kv, window, sinks, scale=None, dO=None, exact_d=False):
         t = Q.dtype
         n, H, d = Q.shape
         Hkv = K.shape[1]
@@ -72,6 +72,8 @@ class Ref:
         D = (g * O).sum(-1, keepdim=True)
         dS = P * (dP - D)
         dD = (g.abs() * tO).sum(-1, keepdim=True) + d * u * (g * O).abs().sum(-1, keepdim=True)
+        if exact_d:       # D = sum P dP in fp32
+            dD = (P * (d * u * (g.abs() @ v.abs().transpose(1, 2)) + e32 * dP.abs())).sum(-1, keepdim=True)
         bS = P * (dD + d * u * (g.abs() @ v.abs().transpose(1, 2))) + (ep + e32) * dS.abs()
 
         def group(x):     # sums over the query heads of each kv head

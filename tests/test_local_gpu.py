@@ -199,6 +199,28 @@ def test_window_backward_many_items(B):
     _backward(BF, 128, 8, 8, B, 150, 150, 150, 0, 0, 0)
 
 
+@pytest.mark.parametrize("d,H,Hkv,T,Tkv,pos0,window,sinks,simt", [
+    (64, 4, 2, 70, 70, 0, 1, 0, False), (128, 8, 2, 100, 100, 0, 1, 1, False), (128, 3, 1, 45, 45, 0, 0, 0, False),
+    (64, 12, 4, 300, 300, 0, 7, 2, False), (64, 2, 2, 64, 64, 0, 64, 0, False), (128, 32, 2, 65, 200, 133, 33, 31, False),
+    (64, 4, 4, 80, 60, 20, 30, 3, False), (64, 4, 2, 70, 70, 0, 5, 0, True)])
+def test_window_backward_of_rows_that_see_few_keys(d, H, Hkv, T, Tkv, pos0, window, sinks, simt):
+    """Where no row sees more than 64 keys, the bf16 gradients do not carry the rounding of O: D = sum P dP in fp32 is
+    off by d 2^-24 sum P |dO||v| + e32 sum P |dP| (e32 as in local_ref, P being off by e32 relative), in place of
+    sum |dO| bound(O).  One visible key: dS is nothing but such errors."""
+    B = 2
+    Q, dO = _rand(1, BF, B, T, H, d), _rand(4, BF, B, T, H, d)
+    K, V = _rand(2, BF, B, Tkv, Hkv, d), _rand(3, BF, B, Tkv, Hkv, d)
+    p = torch.arange(pos0, pos0 + T, device="cuda")
+    assert int(seen(p, Tkv, Tkv, window, sinks).sum(1).max()) <= 64
+    kw = dict(q_pos0=pos0, kv_len=Tkv, force_simt=simt)
+    O, lse = hsa.window_attend(Q, K, V, window, sinks, return_lse=True, **kw)
+    dQ, dK, _ = hsa.window_backward(Q, K, V, O, lse, dO, window, sinks, **kw)
+    for b in range(B):
+        r = Ref(Q[b], K[b], V[b], p, Tkv, window, sinks, None, dO[b], exact_d=True)
+        check(f"dQ[{b}]", dQ[b], r.dQ, r.tdQ)
+        check(f"dK[{b}]", dK[b], r.dK, r.tdK)
+
+
 def test_window_backward_against_differences():
     """The fp32 gradients along random directions against central differences of the fp32 forward.  With step h a
     difference is off by h^2/6 of a third derivative (order 1 here times the sizes below) and by the forward's
