@@ -47,7 +47,7 @@ hsa_status_t shape_of(const hsa_window_t *in, LocArgs *a) {
         return fail(HSA_ERR_INVALID_ARG, "kv_cap=%d is below Tkv=%d", in->kv_cap, in->Tkv);
     if (in->B > 65535) return fail(HSA_ERR_UNSUPPORTED, "B=%d (max 65535)", in->B);
     const int cap = in->kv_cap != 0 ? in->kv_cap : in->Tkv;
-    if (in->q_pos0 + in->Tq > MAX_POS || cap > MAX_POS)
+    if (in->q_pos0 > MAX_POS - (int64_t)in->Tq || cap > MAX_POS)   // the sum itself may not fit 64 bits
         return fail(HSA_ERR_UNSUPPORTED, "positions must stay below 2^30");
     if ((long long)in->B * in->Tq > INT_MAX || (long long)in->B * cap > INT_MAX ||
         (long long)in->B * in->Tq * in->H > (1ll << 33))

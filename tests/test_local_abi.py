@@ -67,6 +67,21 @@ def test_paged_refusals(kw, status):
     assert L.hsa_paged_append(p, None, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, BIG, None) == status
 
 
+@pytest.mark.parametrize("q_pos0", [(1 << 30) - 99, 1 << 62, (1 << 63) - 1, (1 << 63) - 100])
+def test_positions_up_to_the_last_64_bit_one_are_refused(q_pos0):
+    """100 rows from q_pos0 pass 2^30, however their sum is stored (one row less at 2^30 - 99 would fit)."""
+    L = _native.lib()
+    n = ctypes.c_size_t(77)
+    p = ctypes.byref(_window(q_pos0=q_pos0))
+    assert L.hsa_window_workspace_size(p, ctypes.byref(n)) == UNSUPPORTED
+    assert L.hsa_window_backward_workspace_size(p, ctypes.byref(n)) == UNSUPPORTED and n.value == 77
+    assert L.hsa_window_attend(p, PTR, PTR, PTR, PTR, None, PTR, BIG, None) == UNSUPPORTED
+    assert L.hsa_window_backward(p, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, PTR, BIG, None) == UNSUPPORTED
+    r = hsa.make_rope(64)
+    assert L.hsa_rope(ctypes.byref(r), p, None, 0, PTR, PTR, PTR, PTR, None) == UNSUPPORTED
+    assert L.hsa_window_workspace_size(ctypes.byref(_window(q_pos0=(1 << 30) - 100)), ctypes.byref(n)) == 0
+
+
 def _each(fn, args, optional=()):
     """The call with each pointer missing, then misaligned, in turn."""
     for i, a in enumerate(args):
