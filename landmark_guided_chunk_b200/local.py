@@ -77,6 +77,15 @@ def _shape(name, t, want):
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(want)}")
 
 
+def _wide(**ints):
+    """An integer that its 32-bit (pos0, q_pos0: 64-bit) field would be cut to is refused here; a negative one is
+    left to the library."""
+    for name, x in ints.items():
+        bits = 63 if name.endswith("pos0") else 31
+        if x >> bits not in (0, -1):
+            raise ValueError(f"{name}={x} does not fit {bits + 1} bits")
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -116,6 +125,8 @@ def make_rope(rot: int, theta: float = 10000.0, interleaved: bool = False, scali
     two).  Made once per model and kept."""
     if scaling not in _SCALING:
         raise ValueError(f"scaling {scaling!r}: one of {', '.join(_SCALING)}")
+    if (rot | orig_len) >> 31:
+        _wide(rot=rot, orig_len=orig_len)
     r = hsa_rope_t(rot, int(interleaved), _SCALING[scaling], orig_len, theta, factor, low, high, mscale)
     _native.check(_native.lib().hsa_rope_init(_byref(r)), "hsa_rope_init")
     return r
@@ -144,6 +155,8 @@ def rope(r: hsa_rope_t, Q=None, K=None, pos0: int = 0, pos=None, inverse: bool =
         K_out = torch.empty_like(K)
     _shape("Q_out", Q_out, Q.shape if Q is not None else ())
     _shape("K_out", K_out, K.shape if K is not None else ())
+    if pos0 >> 63:
+        _wide(pos0=pos0)
     prob = hsa_window_t(B, T, 0, H, Hkv, d, pos0, 0, 0, 0.0, _dtype(x), 0, 0)
     _call("hsa_rope", x, _byref(r), _byref(prob), _p(pos), int(inverse), _p(Q), _p(K), _p(Q_out), _p(K_out))
     if Q is not None and K is not None:
@@ -158,7 +171,11 @@ def _window(Q, K, window, sinks, q_pos0, kv_len, scale, force_simt):
     if K.dim() != 4 or K.shape[0] != B or K.shape[3] != d:
         raise ValueError(f"K is {tuple(K.shape)}, expected ({B}, Tcap, Hkv, {d})")
     Tcap, Hkv = K.shape[1], K.shape[2]
-    return hsa_window_t(B, Tq, Tcap if kv_len is None else kv_len, H, Hkv, d, q_pos0, window, sinks, scale or 0.0,
+    if kv_len is None:
+        kv_len = Tcap
+    if (window | sinks | kv_len) >> 31 or q_pos0 >> 63:
+        _wide(window=window, sinks=sinks, kv_len=kv_len, q_pos0=q_pos0)
+    return hsa_window_t(B, Tq, kv_len, H, Hkv, d, q_pos0, window, sinks, scale or 0.0,
                         _dtype(Q), _native.HSA_FLAG_SIMT if force_simt else 0, Tcap)
 
 
@@ -215,6 +232,8 @@ def window_backward(Q, K, V, O, lse, dO, window, sinks=0, q_pos0=0, kv_len=None,
 def _paged(H, rows, Kp, table, max_q, max_kv, window, sinks, scale, force_simt):
     npages, page, Hkv, d = Kp.shape
     B, max_pages = table.shape
+    if (max_q | max_kv | window | sinks) >> 31:
+        _wide(max_q=max_q, max_kv=max_kv, window=window, sinks=sinks)
     return hsa_paged_t(B, rows, max_q, max_kv, H, Hkv, d, page, npages, max_pages, window, sinks, scale or 0.0,
                        _dtype(Kp), _native.HSA_FLAG_SIMT if force_simt else 0)
 

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import landmark_guided_chunk_b200 as hsa
-from landmark_guided_chunk_b200 import _native
+from landmark_guided_chunk_b200 import _native, local
 from landmark_guided_chunk_b200._native import hsa_paged_t, hsa_rope_t, hsa_window_t
 from tests.local_ref import inv_freq
 
@@ -182,6 +182,63 @@ def test_binding_refusals():
         hsa.paged_attend(x[0], x, x, i, i[:1], i[None])
     with pytest.raises(ValueError):
         hsa.paged_append(x[0], x[0], x, x, i, i[:1], i[None])
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The binding with its device checks open to CPU tensors, and its library calls recorded in place of made."""
+    made = []
+    monkeypatch.setattr(local, "_check", lambda *a: None)
+    monkeypatch.setattr(local, "_call", lambda name, like, *a: made.append((name, a)))
+    return made
+
+
+def _five(x, i, **kw):
+    """The five calls that take device data, on x as every tensor and i as every index array."""
+    p, l = x[0], torch.zeros(x.shape[:3])
+    w = {k: v for k, v in kw.items() if k in ("window", "sinks", "q_pos0", "kv_len", "ws")}
+    w.setdefault("window", 3)
+    g = {k: v for k, v in kw.items() if k in ("window", "sinks", "max_q", "max_kv", "ws")}
+    return {"window_attend": lambda: hsa.window_attend(x, x, x, **w),
+            "window_backward": lambda: hsa.window_backward(x, x, x, x, l, x, **w),
+            "paged_attend": lambda: hsa.paged_attend(p, x, x, i[:2], i[:1], i[None], **g),
+            "paged_append": lambda: hsa.paged_append(p, p, x, x, i[:2], i[:1], i[None], **({"ws": kw["ws"]} if "ws" in kw else {})),
+            "rope": lambda: hsa.rope(hsa.make_rope(64), x, pos0=kw.get("pos0", 0))}
+
+
+@pytest.mark.parametrize("name,value", [(n, v) for n in ("window", "sinks", "kv_len", "max_q", "max_kv")
+                                        for v in (2 ** 31, 2 ** 32 + 4, -2 ** 31 - 1)] +
+                         [(n, v) for n in ("q_pos0", "pos0") for v in (2 ** 63, 2 ** 64 + 4, -2 ** 63 - 1)])
+def test_binding_integers_are_not_cut_to_their_fields(calls, name, value):
+    """2^32 + 4 in a 32-bit field would be 4: a window of four tokens in place of all."""
+    x, i = torch.zeros(1, 16, 2, 64), torch.zeros(2, dtype=torch.int32)
+    takes = {"window": 3, "sinks": 3, "kv_len": 2, "q_pos0": 2, "max_q": 1, "max_kv": 1, "pos0": 1}[name]
+    refused = 0
+    for call in _five(x, i, **{name: value}).values():
+        try:
+            call()
+        except ValueError as e:
+            assert name in str(e)
+            refused += 1
+    assert refused == takes and len(calls) == 5 - takes
+    if name in ("window", "sinks", "kv_len", "q_pos0"):
+        with pytest.raises(ValueError, match=name):
+            hsa.window_workspace(x, x, **{"window": 3, name: value})
+    if name in ("window", "sinks", "max_q", "max_kv"):
+        with pytest.raises(ValueError, match=name):
+            hsa.paged_workspace(x[0], x, i[None], **{name: value})
+
+
+def test_binding_integers_at_the_ends_of_their_fields(calls):
+    x, i = torch.zeros(1, 16, 2, 64), torch.zeros(2, dtype=torch.int32)
+    for call in _five(x, i, window=2 ** 31 - 1, sinks=2 ** 31 - 1, pos0=2 ** 63 - 1).values():
+        call()
+    assert len(calls) == 5
+    with pytest.raises(hsa.HSAError):       # negative ones are the library's to refuse
+        hsa.window_workspace(x, x, -1)
+    for kw in (dict(rot=2 ** 32 + 64), dict(rot=64, orig_len=2 ** 32 + 64)):
+        with pytest.raises(ValueError):
+            hsa.make_rope(**kw)
 
 
 def test_nothing_to_do_needs_no_pointers():
