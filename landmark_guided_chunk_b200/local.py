@@ -72,6 +72,11 @@ def _ints(like, *names_tensors):
             raise ValueError(f"{name} must be contiguous and on {like.device}")
 
 
+def _ws(like, ws):
+    if ws.get_device() != like.get_device() or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on {like.device}")
+
+
 def _shape(name, t, want):
     if t is not None and t.shape != want:
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(want)}")
@@ -202,6 +207,8 @@ def window_attend(Q, K, V, window, sinks=0, q_pos0=0, kv_len=None, scale=None, O
         O = torch.empty_like(Q)
     if ws is None:
         ws = _workspace("hsa_window_workspace_size", prob, Q.device)
+    else:
+        _ws(Q, ws)
     lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device) if return_lse else None
     _call("hsa_window_attend", Q, _byref(prob), _p(Q), _p(K), _p(V), _p(O), _p(lse), _p(ws), ws.numel())
     return (O, lse) if return_lse else O
@@ -222,6 +229,8 @@ def window_backward(Q, K, V, O, lse, dO, window, sinks=0, q_pos0=0, kv_len=None,
     prob = _window(Q, K, window, sinks, q_pos0, kv_len, scale, force_simt)
     if ws is None:
         ws = _workspace("hsa_window_backward_workspace_size", prob, Q.device)
+    else:
+        _ws(Q, ws)
     _call("hsa_window_backward", Q, _byref(prob), _p(Q), _p(K), _p(V), _p(O), _p(lse), _p(dO), _p(dQ), _p(dK), _p(dV),
           _p(ws), ws.numel())
     return dQ, dK, dV
@@ -270,6 +279,8 @@ def paged_append(k_new, v_new, K_pages, V_pages, q_start, kv_len, table, Q=None,
     prob = _paged(H, rows, K_pages, table, rows, 0, 0, 0, 0.0, False)
     if ws is None:
         ws = torch.zeros(256, dtype=torch.uint8, device=k_new.device)
+    else:
+        _ws(k_new, ws)
     _call("hsa_paged_append", k_new, _byref(prob), None if rope is None else _byref(rope), _p(k_new), _p(v_new), _p(Q),
           _p(Q_out), _p(q_start), _p(kv_len), _p(table), _p(K_pages), _p(V_pages), _p(ws), ws.numel())
     return Q_out if Q is not None else None
@@ -296,6 +307,8 @@ def paged_attend(Q, K_pages, V_pages, q_start, kv_len, table, max_q=None, max_kv
         O = torch.empty_like(Q)
     if ws is None:
         ws = _workspace("hsa_paged_workspace_size", prob, Q.device)
+    else:
+        _ws(Q, ws)
     _call("hsa_paged_attend", Q, _byref(prob), _p(Q), _p(K_pages), _p(V_pages), _p(q_start), _p(kv_len), _p(table),
           _p(O), _p(ws), ws.numel())
     return O

@@ -241,6 +241,29 @@ def test_binding_integers_at_the_ends_of_their_fields(calls):
             hsa.make_rope(**kw)
 
 
+class _OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on device 0, for checks that must not follow its pointer."""
+
+    def get_device(self):
+        return 0
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1 << 20, dtype=torch.uint8),
+                                torch.zeros(1 << 21, dtype=torch.uint8)[::2].as_subclass(_OnDevice)], ids=["cpu", "strided"])
+def test_binding_workspaces(calls, ws):
+    """A workspace on the host, or a strided view, must not reach a kernel as a pointer."""
+    x, i = (torch.zeros(s, dtype=t).as_subclass(_OnDevice) for s, t in (((1, 16, 2, 64), torch.float32), ((2,), torch.int32)))
+    for name, call in _five(x, i, ws=ws).items():
+        if name != "rope":
+            with pytest.raises(ValueError, match="ws"):
+                call()
+    assert not calls
+    good = torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(_OnDevice)
+    for call in _five(x, i, ws=good).values():
+        call()
+    assert len(calls) == 5
+
+
 def test_nothing_to_do_needs_no_pointers():
     L = _native.lib()
     ws = (ctypes.c_char * 1024)()

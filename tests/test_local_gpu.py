@@ -437,6 +437,19 @@ def test_paged_bad_pages_and_lengths():
     assert torch.equal(P.K, K0) and torch.equal(P.V, V0)
 
 
+def test_workspaces_elsewhere_are_refused():
+    P = Pages(BF, 64, 4, 2, [4, 1], [100, 40], 32)
+    Q, K = _rand(1, BF, 1, 9, 4, 64), _rand(2, BF, 1, 9, 2, 64)
+    O, lse = hsa.window_attend(Q, K, K, 3, return_lse=True)
+    for ws in (torch.zeros(1 << 24, dtype=torch.uint8), torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")[::2]):
+        for call in (lambda: hsa.window_attend(Q, K, K, 3, ws=ws),
+                     lambda: hsa.window_backward(Q, K, K, O, lse, Q, 3, ws=ws),
+                     lambda: hsa.paged_attend(P.Q, P.K, P.V, P.q_start, P.kv_len, P.table, ws=ws),
+                     lambda: hsa.paged_append(P.k, P.v, P.K, P.V, P.q_start, P.kv_len, P.table, ws=ws)):
+            with pytest.raises(ValueError, match="ws"):
+                call()
+
+
 def test_paged_shared_pages():
     """A forked prefix: two sequences whose tables name the same pages, one of them twice in a row of the table."""
     P = Pages(BF, 128, 8, 2, [1, 40, 1], [200, 200, 96], 32)
