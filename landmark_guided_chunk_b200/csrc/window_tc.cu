@@ -50,7 +50,8 @@ struct Share {
 
 struct __align__(8) Bars {
     uint64_t q_full[2][2], q_empty[2][2], kv_full[8], kv_empty[8], land[8];   // q: [buffer][tile]
-    uint64_t s_full[2], p_full[2][2], o_full[2], out_full[2], done;           // p: [tile][half of its keys]
+    uint64_t s_full[2], p_full[2][2], o_full[2], done;                        // p: [tile][half of its keys]
+    uint64_t out_full[2][2];      // [Q buffer][tile]: the next item's output may be ready before this one's is looked for
     uint32_t tmem_base;
     int abort;
     Share share;
@@ -285,10 +286,10 @@ __global__ void __launch_bounds__(NT, 1)
                 mbar_init(&bar->q_full[x][t], 1);
                 mbar_init(&bar->q_empty[x][t], 1);
                 mbar_init(&bar->p_full[t][x], 4);
+                mbar_init(&bar->out_full[x][t], 4);
             }
             mbar_init(&bar->s_full[t], 1);
             mbar_init(&bar->o_full[t], 1);
-            mbar_init(&bar->out_full[t], 4);
         }
         for (int s = 0; s < C::NST; ++s) {
             mbar_init(&bar->kv_full[s], 1);
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(NT, 1)
             if (any) {
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->out_full[t]);
+                if (lane == 0) mbar_arrive(&bar->out_full[na % C::QB][t]);
                 ++na;
             }
             tc_fence_before();   // these reads come before the next item's product into O (through p_full)
@@ -666,8 +667,9 @@ __global__ void __launch_bounds__(NT, 1)
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 const int x = na++ % C::QB;
                 for (int t = 0; t < it.ntile; ++t) {
-                    if (!(ok = mbar_wait(&bar->out_full[t], par >> t & 1, abort, status, ITEM_WAIT_NS))) break;
-                    par ^= 1u << t;
+                    const int bit = 2 * x + t;
+                    if (!(ok = mbar_wait(&bar->out_full[x][t], par >> bit & 1, abort, status, ITEM_WAIT_NS))) break;
+                    par ^= 1u << bit;
                     if (lane == 0) {
                         if (it.slot < 0 && it.t0 + (t + 1) * tok <= it.s.n) {
                             for (int y = 0; y < C::NBX; ++y)
