@@ -60,9 +60,29 @@ struct PollLimit {
     }
 };
 
-// Bound of a wait that lasts a whole work item (a row block over all its keys), not a tile: 16M keys take a quarter
-// of a second.
-constexpr uint64_t ITEM_WAIT_NS = 30000000000ull;
+// As mbar_wait, for a role that runs ahead of the others: through tiles and items that it has no part in, to a phase
+// that may be minutes away.  The limit counts from the last advance of *step, the number of tiles that the loader has
+// issued: the loader's own waits have the plain limit, and what it has issued is at most a ring away.
+__device__ __forceinline__ bool mbar_wait_ahead(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *status,
+                                                const volatile uint32_t *step) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t seen = *step;
+    uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (mbar_try_wait_suspend(bar, parity, SUSPEND_NS)) return true;
+        if (*abort) return false;
+        const uint32_t now = *step;
+        const uint64_t t = globaltimer_ns();
+        if (now != seen) {
+            seen = now;
+            t0 = t;
+        } else if (t - t0 > WAIT_LIMIT_NS) {
+            *abort = 1;
+            atomicOr(status, DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {

@@ -168,6 +168,7 @@ struct __align__(8) DqBars {
     uint64_t q_full, q_empty, k_full[KST], k_empty[KST], land[KST], v_full[VST], v_empty[VST];
     uint64_t s_full[QSB], s_empty[QSB], ds_full[QSB], dp_full[2], dp_empty[2], dq_full, dq_empty, done[4];   // [TMEM buffer]
     uint32_t tmem_base;
+    uint32_t step;   // K tiles that the loader has issued
     int abort;
 };
 
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(NTQ, 1)
         for (int s = 0; s < 4; ++s) mbar_init(&bar->done[s], 1);
         mbar_init(&bar->dq_full, 1);
         mbar_init(&bar->dq_empty, 16);
+        bar->step = 0;
         bar->abort = 0;
         fence_mbar_init();
     }
@@ -330,8 +332,9 @@ __global__ void __launch_bounds__(NTQ, 1)
                             tma_load_3d(sK + ks * C::RT + x * RR * 128, &tmK, 64 * x, it.j, row, full);
                     }
                     ++nk;
+                    if (lane == 0) *(volatile uint32_t *)&bar->step = nk;
                     if (i == 0) {
-                        if (nq > 0 && !(ok = mbar_wait(&bar->q_empty, (nq - 1) & 1, abort, status, ITEM_WAIT_NS))) break;
+                        if (nq > 0 && !(ok = mbar_wait(&bar->q_empty, (nq - 1) & 1, abort, status))) break;
                         ++nq;
                         if (lane == 0) {
                             mbar_expect_tx(&bar->q_full, 2 * qbytes);
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(NTQ, 1)
                     const int used = it.tl.end(i) - it.tl.start(i), width = it.tl.width(i);
                     if (used == width) continue;
                     const uint32_t ks = nk % KST;
-                    if (!(ok = mbar_wait(&bar->land[ks], land_par >> ks & 1, abort, status))) break;
+                    if (!(ok = mbar_wait_ahead(&bar->land[ks], land_par >> ks & 1, abort, status, &bar->step))) break;
                     land_par ^= 1u << ks;
                     for (int r = used + (lane >> 3); r < width; r += 4)
                         for (int x = 0; x < C::NBX; ++x)
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(NTK, 1)
             for (int idx = blockIdx.x; idx < nitems && ok; idx += gridDim.x) {
                 const KvItem it = kv_item(w, idx, tok);
                 if (it.nt == 0) continue;
-                if (ni > 0 && !(ok = mbar_wait(&bar->kv_empty, (ni - 1) & 1, abort, status, ITEM_WAIT_NS))) break;
+                if (ni > 0 && !(ok = mbar_wait(&bar->kv_empty, (ni - 1) & 1, abort, status))) break;
                 ++ni;
                 if (lane == 0) {
                     mbar_expect_tx(&bar->kv_full, 2 * C::TILE);

@@ -53,6 +53,7 @@ struct __align__(8) Bars {
     uint64_t s_full[2], p_full[2][2], o_full[2], done;                        // p: [tile][half of its keys]
     uint64_t out_full[2][2];      // [Q buffer][tile]: the next item's output may be ready before this one's is looked for
     uint32_t tmem_base;
+    uint32_t step;                // K and V tiles that the loader has issued
     int abort;
     Share share;
     int row[2][MR];               // token of each row's output (-1: padding)
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(NT, 1)
     uint8_t *sKV = base + 2 * C::QB * C::TILE;   // NST tiles
     Bars *bar = reinterpret_cast<Bars *>(sKV + C::NST * C::TILE);
     volatile int *abort = &bar->abort;
+    volatile uint32_t *step = &bar->step;
     uint32_t *status = a.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&bar->land[s], 1);
         }
         mbar_init(&bar->done, 1);
+        bar->step = 0;
         bar->abort = 0;
         fence_mbar_init();
     }
@@ -344,7 +347,8 @@ __global__ void __launch_bounds__(NT, 1)
             uint64_t l2 = 0;   // row sum in two parts
             for (int i = i0; i < i1; ++i, ++n) {
                 const int u0 = tl.start(i), nc = tl.width(i);
-                if (!(ok = mbar_wait(&bar->s_full[t], n & 1, abort, status))) break;
+                // (the second tile's warps have passed over items of one tile)
+                if (!(ok = mbar_wait_ahead(&bar->s_full[t], n & 1, abort, status, step))) break;
                 tc_fence_after();
                 uint32_t sr[4][32];
                 const int end = min(we, (i < tl.nst ? tl.send : tl.hi) - 1);   // keys past a cut tile belong to others
@@ -535,13 +539,14 @@ __global__ void __launch_bounds__(NT, 1)
                                 tma_load_3d(dst + x * 16384, kv ? &tmV : &tmK, 64 * x, it.j, row, full);
                         }
                         ++nkv;
+                        if (lane == 0) *step = nkv;
                         if (kv == 0 && i == it.i0) {
                             // the item's query tiles, into the buffer that the item before last has left
                             const int x = na++ % C::QB;
                             for (int t = 0; t < it.ntile && ok; ++t) {
                                 const uint32_t bit = 1u << (2 * x + t);
                                 if ((qused & bit) &&
-                                    !(ok = mbar_wait(&bar->q_empty[x][t], (qpar & bit) ? 0 : 1, abort, status, ITEM_WAIT_NS)))
+                                    !(ok = mbar_wait(&bar->q_empty[x][t], (qpar & bit) ? 0 : 1, abort, status)))
                                     break;
                                 qused |= bit;
                                 qpar ^= bit;
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(NT, 1)
                 const int x = na++ % C::QB;
                 for (int t = 0; t < it.ntile; ++t) {
                     const int bit = 2 * x + t;
-                    if (!(ok = mbar_wait(&bar->out_full[x][t], par >> bit & 1, abort, status, ITEM_WAIT_NS))) break;
+                    if (!(ok = mbar_wait_ahead(&bar->out_full[x][t], par >> bit & 1, abort, status, step))) break;
                     par ^= 1u << bit;
                     if (lane == 0) {
                         if (it.slot < 0 && it.t0 + (t + 1) * tok <= it.s.n) {
@@ -694,7 +699,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (!it.tl.has_dead(i)) continue;
                     const int u0 = it.tl.start(i), width = it.tl.width(i);
                     const int s = (nkv + 1) % C::NST;
-                    if (!(ok = mbar_wait(&bar->land[s], land_par >> s & 1, abort, status))) break;
+                    if (!(ok = mbar_wait_ahead(&bar->land[s], land_par >> s & 1, abort, status, step))) break;
                     land_par ^= 1u << s;
                     uint8_t *v = sKV + s * C::TILE;
                     // 8 lanes per 128-byte row

@@ -242,6 +242,56 @@ def test_window_backward_against_differences():
         assert abs(want - got) <= noise + 1e-3 * abs(want), (i, want, got, noise)
 
 
+def _far_tail(T):
+    """Two sequences of T tokens, of which the last 300 see old keys at scores 512 below the others': what they bring
+    is 2^-700, nothing, and a row's result is that over the last 300 keys alone."""
+    Q, K, V = (_rand(i, BF, 2, T, 1, 64) for i in range(3))
+    Q[..., 0] = 16
+    K[:, :-300] = 0
+    K[..., 0] = 0
+    K[:, :-300, :, 0] = -256        # 16 (-256) / 8
+    return Q, K, V
+
+
+def _tail(b, n, *xs):
+    return [x[b, -n:] for x in xs]
+
+
+def test_a_call_of_seconds():
+    """A helper warp that has no part in a sequence's whole tiles waits for the next ragged one, here for the whole
+    first sequence: more than the limit of one second that a step has."""
+    Q, K, V = _far_tail(3_000_007)
+    ws = hsa.window_workspace(Q, K, 0)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    O, lse = hsa.window_attend(Q, K, V, 0, O=torch.full_like(Q, math.nan), ws=ws, return_lse=True)
+    end.record()
+    _clean(ws)
+    assert start.elapsed_time(end) > 2400       # else the sizes above are too small to show it
+    assert not bool(O.isnan().any())
+    p = torch.arange(200, 300, device="cuda")
+    for b in range(2):
+        r = Ref(*_tail(b, 100, Q), *_tail(b, 300, K, V), p, 300, 0, 0)
+        check(f"O[{b}]", O[b, -100:], r.O, r.tO)
+        check(f"lse[{b}]", lse[b, -100:], r.lse, r.tlse)
+
+
+def test_a_backward_of_seconds():
+    """As above: the helper of dQ waits for the second sequence's ragged tile."""
+    Q, K, V = _far_tail(2_200_007)
+    dO = _rand(4, BF, *Q.shape)
+    ws = hsa.window_workspace(Q, K, 0, backward=True)
+    O, lse = hsa.window_attend(Q, K, V, 0, ws=ws, return_lse=True)
+    out = tuple(torch.full_like(x, math.nan) for x in (Q, K, V))
+    dQ, dK, dV = hsa.window_backward(Q, K, V, O, lse, dO, 0, out=out, ws=ws)
+    _clean(ws)
+    assert not any(bool(x.isnan().any()) for x in out)
+    p = torch.arange(200, 300, device="cuda")
+    for b in range(2):
+        r = Ref(*_tail(b, 100, Q), *_tail(b, 300, K, V), p, 300, 0, 0, None, *_tail(b, 100, dO))
+        check(f"dQ[{b}]", dQ[b, -100:], r.dQ, r.tdQ)
+
+
 def test_window_without_queries_or_keys():
     K = torch.zeros(2, 5, 2, 64, device="cuda")
     Q = torch.zeros(2, 0, 4, 64, device="cuda")

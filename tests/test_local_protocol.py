@@ -6,8 +6,12 @@ ring, an item's Q tiles into one of two buffers), the MMA warp, four softmax war
 dead V rows, and the output warp, which stores an item's output from its Q buffer and frees it.  This model replays each
 role with the kernel's phase arithmetic under random interleavings and completion delays, with one role at a time made
 slow, and checks that every role finishes and that every waiter tests its barrier only while the awaited phase is open
-or the one just completed: a wait that knows only a parity misreads anything else.  A change to the kernel's barriers,
-counts or phases has to be mirrored here.
+or the one just completed: a wait that knows only a parity misreads anything else.
+
+Waits are bounded in time.  A wait with the plain limit may only span a ring's worth of the loader's tiles; the roles
+that pass over tiles without a wait of their own (the helper, the output warp, the softmax of the second row tile) count
+their limit from the loader's last tile (mbar_wait_ahead).  A change to the kernel's barriers, counts, phases or limits
+has to be mirrored here.
 """
 import random
 
@@ -29,8 +33,9 @@ class Bar:
 class Cta:
     """items: (row tiles, [tile has dead V rows, ...]).  Each role is a generator that yields (barrier, phase) waits."""
 
-    def __init__(self, items, nst, rng, out_buffers=QB):
-        self.items, self.nst, self.rng, self.outs = items, nst, rng, out_buffers
+    def __init__(self, items, nst, rng, out_buffers=QB, ahead=("helper", "output", "softmax")):
+        self.items, self.nst, self.rng, self.outs, self.ahead = items, nst, rng, out_buffers, ahead
+        self.step = 0                      # tiles that the loader has issued
         def grid(name, count, *dims):
             if not dims:
                 return Bar(name, count)
@@ -57,6 +62,7 @@ class Cta:
                         yield self.kv_empty[s], nkv // self.nst - 1
                     self.tma.append([self.land[s] if kv and dead else self.kv_full[s]])
                     nkv += 1
+                    self.step = nkv
                     if kv == 0 and i == 0:
                         x, na = na % QB, na + 1
                         for t in range(ntile):
@@ -141,6 +147,7 @@ class Cta:
                 roles[f"softmax{t}.{w}"] = self.softmax(t)
         slow = self.rng.choice(list(roles) + ["tma", "mma", ""])
         waits = {r: None for r in roles}       # None: ready to run on
+        since = {r: 0 for r in roles}
         idle = 0
         while roles:
             who = self.rng.choice(list(roles) + ["tma", "mma"])
@@ -160,11 +167,15 @@ class Cta:
             if waits[who] is not None:
                 bar, phase = waits[who]
                 assert phase <= bar.phase <= phase + 1, f"{who} tests phase {phase} of {bar.name} in phase {bar.phase}"
-                if bar.phase == phase:
+                if bar.phase == phase:      # the kernel looks at its limit after a failed test
+                    # (the softmax's o_full waits have the plain one)
+                    if not who.startswith(self.ahead) or bar in self.o_full:
+                        assert self.step - since[who] <= 2 * self.nst, f"{who}: limit spans {self.step - since[who]} tiles"
                     continue
             idle = 0
             try:
                 waits[who] = next(roles[who])
+                since[who] = self.step
             except StopIteration:
                 del roles[who], waits[who]
 
@@ -189,3 +200,12 @@ def test_one_output_barrier_per_row_tile_would_not_do():
         for seed in range(1500):
             rng = random.Random(seed)
             Cta(_items(rng), 3, rng, out_buffers=1).run()
+
+
+@pytest.mark.parametrize("role", ["helper", "output", "softmax"])
+def test_roles_that_run_ahead_need_their_own_limit(role):
+    ahead = tuple({"helper", "output", "softmax"} - {role})
+    with pytest.raises(AssertionError, match=f"{role}.*: limit spans"):
+        for seed in range(1500):
+            rng = random.Random(seed)
+            Cta(_items(rng), 3, rng, ahead=ahead).run()
