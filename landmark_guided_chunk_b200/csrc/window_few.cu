@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(NT) window_few_kernel(const __grid_constant__ 
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
 
+    int issued = 0;   // producer: tiles whose loads are under way or have landed
     if (warp == NW) {
         // ---------------------------------------------------------------- producer
         for (int i = i0; i < i1; ++i) {
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(NT) window_few_kernel(const __grid_constant__ 
                 if (x >= 0) row = (int)x;
             }
             if (n >= NST && !mbar_wait(&bar->empty[st], (n / NST - 1) & 1, abort, a.status)) break;
+            ++issued;
             if (lane == 0) mbar_expect_tx(&bar->full[st], (uint32_t)(nbox * psize) * 128u * 2 * C::NBX);
             __syncwarp();
             if (lane < nbox) {
@@ -261,8 +263,8 @@ __global__ void __launch_bounds__(NT) window_few_kernel(const __grid_constant__ 
     }
     __syncthreads();
     if (*abort) {   // loads may still be in flight into the ring: leave it alone until they have landed
-        if (warp == NW && lane == 0)
-            for (int x = 0; x < NST; ++x) mbar_drain(&bar->full[x], 0);
+        if (warp == NW)
+            for (int x = 0; x < NST && x < issued; ++x) mbar_drain(&bar->full[x], ((issued - 1 - x) / NST) & 1);
     } else if (warp < NW) {
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) {

@@ -209,3 +209,27 @@ def test_roles_that_run_ahead_need_their_own_limit(role):
         for seed in range(1500):
             rng = random.Random(seed)
             Cta(_items(rng), 3, rng, ahead=ahead).run()
+
+
+def _drained(issued, landed, nst, parity_of):
+    """Whether a producer that has issued that many tiles into its ring, the first `landed` of which have arrived (and
+    been consumed as far as a refill needs), would go on from its drain: a wait by parity passes unless the open phase
+    has it."""
+    phase = [len([i for i in range(landed) if i % nst == x]) for x in range(nst)]
+    return all(phase[x] & 1 != parity_of(issued, x, nst) for x in range(nst) if parity_of(issued, x, nst) is not None)
+
+
+def _last_use(issued, x, nst):
+    """window_few_kernel on an expired wait: the phase of a stage's last use; unused stages have none."""
+    return (issued - 1 - x) // nst & 1 if x < issued else None
+
+
+@pytest.mark.parametrize("nst", [3, 4, 6])
+def test_a_producer_that_gives_up_waits_for_its_loads(nst):
+    """Loads that are still in flight when the CTA ends would land in the next one's shared memory."""
+    for issued in range(4 * nst):
+        for landed in range(max(0, issued - nst), issued + 1):
+            assert _drained(issued, landed, nst, _last_use) == (landed == issued), (issued, landed)
+    # parity 0 for every stage passes with the second use still in flight, and waits on stages without a load
+    zero = lambda issued, x, nst: 0    # noqa: E731
+    assert _drained(2 * nst, nst, nst, zero) and not _drained(1, 1, nst, zero)
