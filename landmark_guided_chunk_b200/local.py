@@ -63,18 +63,18 @@ def _check(like, *ts):
 _I32 = torch.int32
 
 
-def _ints(like, *names_tensors):
+def _ints(like, **tensors):
     dev = like.get_device()
-    for name, t in names_tensors:
+    for t in tensors.values():
+        if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+            break
+    else:
+        return
+    for name, t in tensors.items():
         if t.dtype is not _I32:
             raise TypeError(f"{name} must be int32, got {t.dtype}")
         if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and on {like.device}")
-
-
-def _ws(like, ws):
-    if ws.get_device() != like.get_device() or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous and on {like.device}")
 
 
 def _shape(name, t, want):
@@ -98,12 +98,16 @@ def _p(t):
 _fns = {}   # the library's functions by name
 
 
-def _call(name, like, *args):
+def _call(name, like, *args, ws=None):
     """One library call on the current stream of `like`'s device, with that device current."""
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_native.lib(), name)
     index = like.get_device()
+    if ws is not None:
+        if ws.get_device() != index or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous and on {like.device}")
+        args += (ws.data_ptr(), ws.numel())
     if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
@@ -152,7 +156,7 @@ def rope(r: hsa_rope_t, Q=None, K=None, pos0: int = 0, pos=None, inverse: bool =
         if H % Hkv:   # the heads are independent here: any two counts are fine, each in its own launch
             return (rope(r, Q, None, pos0, pos, inverse, Q_out), rope(r, None, K, pos0, pos, inverse, None, K_out))
     if pos is not None:
-        _ints(x, ("pos", pos))
+        _ints(x, pos=pos)
         _shape("pos", pos, (B, T))
     if Q is not None and Q_out is None:
         Q_out = torch.empty_like(Q)
@@ -207,10 +211,8 @@ def window_attend(Q, K, V, window, sinks=0, q_pos0=0, kv_len=None, scale=None, O
         O = torch.empty_like(Q)
     if ws is None:
         ws = _workspace("hsa_window_workspace_size", prob, Q.device)
-    else:
-        _ws(Q, ws)
     lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device) if return_lse else None
-    _call("hsa_window_attend", Q, _byref(prob), _p(Q), _p(K), _p(V), _p(O), _p(lse), _p(ws), ws.numel())
+    _call("hsa_window_attend", Q, _byref(prob), _p(Q), _p(K), _p(V), _p(O), _p(lse), ws=ws)
     return (O, lse) if return_lse else O
 
 
@@ -229,10 +231,8 @@ def window_backward(Q, K, V, O, lse, dO, window, sinks=0, q_pos0=0, kv_len=None,
     prob = _window(Q, K, window, sinks, q_pos0, kv_len, scale, force_simt)
     if ws is None:
         ws = _workspace("hsa_window_backward_workspace_size", prob, Q.device)
-    else:
-        _ws(Q, ws)
     _call("hsa_window_backward", Q, _byref(prob), _p(Q), _p(K), _p(V), _p(O), _p(lse), _p(dO), _p(dQ), _p(dK), _p(dV),
-          _p(ws), ws.numel())
+          ws=ws)
     return dQ, dK, dV
 
 
@@ -261,7 +261,7 @@ def paged_append(k_new, v_new, K_pages, V_pages, q_start, kv_len, table, Q=None,
     rope (make_rope) K is rotated to its position on the way, and Q [rows,H,d] too.  Returns Q_out (Q rotated; a
     new tensor unless given; rows behind the last sequence are not written), or None without Q."""
     _check(k_new, v_new, K_pages, V_pages, Q, Q_out)
-    _ints(k_new, ("q_start", q_start), ("kv_len", kv_len), ("table", table))
+    _ints(k_new, q_start=q_start, kv_len=kv_len, table=table)
     rows, Hkv, d = k_new.shape
     npages, page, B = K_pages.shape[0], K_pages.shape[1], table.shape[0]
     _shape("v_new", v_new, k_new.shape)
@@ -279,10 +279,8 @@ def paged_append(k_new, v_new, K_pages, V_pages, q_start, kv_len, table, Q=None,
     prob = _paged(H, rows, K_pages, table, rows, 0, 0, 0, 0.0, False)
     if ws is None:
         ws = torch.zeros(256, dtype=torch.uint8, device=k_new.device)
-    else:
-        _ws(k_new, ws)
     _call("hsa_paged_append", k_new, _byref(prob), None if rope is None else _byref(rope), _p(k_new), _p(v_new), _p(Q),
-          _p(Q_out), _p(q_start), _p(kv_len), _p(table), _p(K_pages), _p(V_pages), _p(ws), ws.numel())
+          _p(Q_out), _p(q_start), _p(kv_len), _p(table), _p(K_pages), _p(V_pages), ws=ws)
     return Q_out if Q is not None else None
 
 
@@ -293,7 +291,7 @@ def paged_attend(Q, K_pages, V_pages, q_start, kv_len, table, max_q=None, max_kv
     rows, and what a table row can hold); the closer they are, the better the work is split.  Returns O; rows
     behind the last sequence are not written."""
     _check(Q, K_pages, V_pages, O)
-    _ints(Q, ("q_start", q_start), ("kv_len", kv_len), ("table", table))
+    _ints(Q, q_start=q_start, kv_len=kv_len, table=table)
     rows, H, d = Q.shape
     B = table.shape[0]
     _shape("V_pages", V_pages, K_pages.shape)
@@ -307,8 +305,6 @@ def paged_attend(Q, K_pages, V_pages, q_start, kv_len, table, max_q=None, max_kv
         O = torch.empty_like(Q)
     if ws is None:
         ws = _workspace("hsa_paged_workspace_size", prob, Q.device)
-    else:
-        _ws(Q, ws)
     _call("hsa_paged_attend", Q, _byref(prob), _p(Q), _p(K_pages), _p(V_pages), _p(q_start), _p(kv_len), _p(table),
-          _p(O), _p(ws), ws.numel())
+          _p(O), ws=ws)
     return O

@@ -188,22 +188,40 @@ def test_binding_refusals():
 def calls(monkeypatch):
     """The binding with its device checks open to CPU tensors, and its library calls recorded in place of made."""
     made = []
+
+    class Library(dict):
+        def get(self, name):
+            return lambda *a: made.append((name, a))
+
     monkeypatch.setattr(local, "_check", lambda *a: None)
-    monkeypatch.setattr(local, "_call", lambda name, like, *a: made.append((name, a)))
+    monkeypatch.setattr(local, "_fns", Library())
+    monkeypatch.setattr(local, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(local, "_current_device", lambda: 0)
     return made
 
 
-def _five(x, i, **kw):
-    """The five calls that take device data, on x as every tensor and i as every index array."""
+class _OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on device 0, for checks that must not follow its pointer."""
+
+    def get_device(self):
+        return 0
+
+
+def _tensors():
+    return (torch.zeros(s, dtype=t).as_subclass(_OnDevice) for s, t in (((1, 16, 2, 64), torch.float32), ((2,), torch.int32)))
+
+
+def _five(x, i, ws=None, pos0=0, **kw):
+    """The calls that take device data, on x as every tensor and i as every index array."""
     p, l = x[0], torch.zeros(x.shape[:3])
-    w = {k: v for k, v in kw.items() if k in ("window", "sinks", "q_pos0", "kv_len", "ws")}
-    w.setdefault("window", 3)
-    g = {k: v for k, v in kw.items() if k in ("window", "sinks", "max_q", "max_kv", "ws")}
-    return {"window_attend": lambda: hsa.window_attend(x, x, x, **w),
-            "window_backward": lambda: hsa.window_backward(x, x, x, x, l, x, **w),
-            "paged_attend": lambda: hsa.paged_attend(p, x, x, i[:2], i[:1], i[None], **g),
-            "paged_append": lambda: hsa.paged_append(p, p, x, x, i[:2], i[:1], i[None], **({"ws": kw["ws"]} if "ws" in kw else {})),
-            "rope": lambda: hsa.rope(hsa.make_rope(64), x, pos0=kw.get("pos0", 0))}
+    ws = torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(_OnDevice) if ws is None else ws
+    w = {"window": 3, **{k: v for k, v in kw.items() if k in ("window", "sinks", "q_pos0", "kv_len")}}
+    g = {k: v for k, v in kw.items() if k in ("window", "sinks", "max_q", "max_kv")}
+    return {"window_attend": lambda: hsa.window_attend(x, x, x, ws=ws, **w),
+            "window_backward": lambda: hsa.window_backward(x, x, x, x, l, x, ws=ws, **w),
+            "paged_attend": lambda: hsa.paged_attend(p, x, x, i[:2], i[:1], i[None], ws=ws, **g),
+            "paged_append": lambda: hsa.paged_append(p, p, x, x, i[:2], i[:1], i[None], ws=ws),
+            "rope": lambda: hsa.rope(hsa.make_rope(64), x, pos0=pos0)}
 
 
 @pytest.mark.parametrize("name,value", [(n, v) for n in ("window", "sinks", "kv_len", "max_q", "max_kv")
@@ -211,7 +229,7 @@ def _five(x, i, **kw):
                          [(n, v) for n in ("q_pos0", "pos0") for v in (2 ** 63, 2 ** 64 + 4, -2 ** 63 - 1)])
 def test_binding_integers_are_not_cut_to_their_fields(calls, name, value):
     """2^32 + 4 in a 32-bit field would be 4: a window of four tokens in place of all."""
-    x, i = torch.zeros(1, 16, 2, 64), torch.zeros(2, dtype=torch.int32)
+    x, i = _tensors()
     takes = {"window": 3, "sinks": 3, "kv_len": 2, "q_pos0": 2, "max_q": 1, "max_kv": 1, "pos0": 1}[name]
     refused = 0
     for call in _five(x, i, **{name: value}).values():
@@ -230,7 +248,7 @@ def test_binding_integers_are_not_cut_to_their_fields(calls, name, value):
 
 
 def test_binding_integers_at_the_ends_of_their_fields(calls):
-    x, i = torch.zeros(1, 16, 2, 64), torch.zeros(2, dtype=torch.int32)
+    x, i = _tensors()
     for call in _five(x, i, window=2 ** 31 - 1, sinks=2 ** 31 - 1, pos0=2 ** 63 - 1).values():
         call()
     assert len(calls) == 5
@@ -241,25 +259,17 @@ def test_binding_integers_at_the_ends_of_their_fields(calls):
             hsa.make_rope(**kw)
 
 
-class _OnDevice(torch.Tensor):
-    """A CPU tensor that says it is on device 0, for checks that must not follow its pointer."""
-
-    def get_device(self):
-        return 0
-
-
 @pytest.mark.parametrize("ws", [torch.zeros(1 << 20, dtype=torch.uint8),
                                 torch.zeros(1 << 21, dtype=torch.uint8)[::2].as_subclass(_OnDevice)], ids=["cpu", "strided"])
 def test_binding_workspaces(calls, ws):
     """A workspace on the host, or a strided view, must not reach a kernel as a pointer."""
-    x, i = (torch.zeros(s, dtype=t).as_subclass(_OnDevice) for s, t in (((1, 16, 2, 64), torch.float32), ((2,), torch.int32)))
+    x, i = _tensors()
     for name, call in _five(x, i, ws=ws).items():
         if name != "rope":
             with pytest.raises(ValueError, match="ws"):
                 call()
     assert not calls
-    good = torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(_OnDevice)
-    for call in _five(x, i, ws=good).values():
+    for call in _five(x, i).values():
         call()
     assert len(calls) == 5
 
