@@ -26,9 +26,10 @@ __all__ = ["make_rope", "rope", "window_workspace", "window_attend", "window_bac
 _DT = {torch.float32: _native.HSA_F32, torch.bfloat16: _native.HSA_BF16}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 _byref = ctypes.byref
-# torch.cuda.current_stream(index).cuda_stream and current_device() without the objects and checks around them
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# torch.cuda.current_stream(index).cuda_stream and current_device() without the objects and checks around them; a
+# torch without CUDA has neither, and no tensor that would get as far
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _dtype(t):

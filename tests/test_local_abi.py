@@ -2,6 +2,9 @@
 entry points (an invalid call launches nothing, so no GPU is needed)."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -272,6 +275,26 @@ def test_binding_workspaces(calls, ws):
     for call in _five(x, i).values():
         call()
     assert len(calls) == 5
+
+
+def test_the_package_imports_on_a_torch_without_cuda():
+    """build.py, inputs, dp and sharded are for machines without a GPU as well."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import landmark_guided_chunk_b200 as hsa
+from landmark_guided_chunk_b200 import build, dp, inputs, sharded
+x = torch.zeros(1, 4, 2, 64)
+try:
+    hsa.window_attend(x, x, x, 3)
+except ValueError as e:
+    print("refused:", e)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused: all tensors must be CUDA tensors" in r.stdout, r.stderr[-2000:]
 
 
 def test_nothing_to_do_needs_no_pointers():
