@@ -432,8 +432,9 @@ HSA_API hsa_status_t hsa_rope_init(hsa_rope_t *rope);
  * pos[b][t] (int32, device) or, with pos NULL, at q_pos0 + t.  The angle is taken in fp64 and reduced
  * to one turn before its fp32 sine, so positions of millions keep their accuracy.  inverse != 0
  * applies the transpose (-sin), which is the gradient's rotation.  Qr may be Q and Kr may be K;
- * other overlaps are not allowed.  Of *p: B, Tq, H, Hkv, d, q_pos0, dtype.  At most
- * 16383 heads in a call (hsa_paged_append: H + 2 Hkv).  No workspace.
+ * other overlaps are not allowed.  Of *p: B, Tq, H, Hkv, d, q_pos0, dtype.  The two head counts are
+ * independent here (no group limit), at most 16383 heads in a call (hsa_paged_append: H + 2 Hkv).
+ * No workspace.
  */
 HSA_API hsa_status_t hsa_rope(const hsa_rope_t *rope, const hsa_window_t *p, const int32_t *pos, int inverse,
                               const void *Q, const void *K, void *Qr, void *Kr, void *stream);

@@ -383,8 +383,8 @@ hsa_status_t hsa_rope_init(hsa_rope_t *r) {
 
 namespace {
 
-hsa_status_t check_head_count(int heads) {
-    if (heads > 16383) return fail(HSA_ERR_UNSUPPORTED, "%d heads in one call (max 16383)", heads);
+hsa_status_t check_head_count(long long heads) {
+    if (heads > 16383) return fail(HSA_ERR_UNSUPPORTED, "%lld heads in one call (max 16383)", heads);
     return HSA_OK;
 }
 
@@ -412,16 +412,17 @@ hsa_status_t hsa_rope(const hsa_rope_t *rope, const hsa_window_t *prob, const in
     hsa_window_t pr{};   // the fields that count here; the others may hold anything
     pr.B = prob->B;
     pr.Tq = prob->Tq;
-    pr.H = prob->H;
-    pr.Hkv = prob->Hkv;
+    pr.H = pr.Hkv = 1;   // the two head counts have nothing to do with each other here
     pr.d = prob->d;
     pr.q_pos0 = prob->q_pos0;
     pr.dtype = prob->dtype;
     LocArgs a;
     HSA_TRY(shape_of(&pr, &a));
+    const long long H = prob->H, Hkv = prob->Hkv;
+    if (H < 1 || Hkv < 1) return fail(HSA_ERR_INVALID_ARG, "H, Hkv must be >= 1 (H=%lld Hkv=%lld)", H, Hkv);
     RopeArgs r;
     HSA_TRY(rope_args(rope, a.d, &r));
-    HSA_TRY(check_head_count((Q ? a.H : 0) + (K ? a.Hkv : 0)));
+    HSA_TRY(check_head_count((Q ? H : 0) + (K ? Hkv : 0)));
     const bool rows = a.rows > 0;
     if (rows && !Q && !K) return fail(HSA_ERR_INVALID_ARG, "Q and K are both NULL");
     HSA_TRY(need(Q, Q != nullptr, "Q"));
@@ -431,7 +432,7 @@ hsa_status_t hsa_rope(const hsa_rope_t *rope, const hsa_window_t *prob, const in
     if (pos) HSA_TRY(need4(pos, "pos"));
     if (!rows) return HSA_OK;
     if (inverse) r.sgn = -1.f;
-    cudaError_t e = launch_rope(r, prob->dtype, a.B, a.max_q, a.H, a.Hkv, a.d, a.q_pos0, pos, Q, K, Qr, Kr,
+    cudaError_t e = launch_rope(r, prob->dtype, a.B, a.max_q, (int)H, (int)Hkv, a.d, a.q_pos0, pos, Q, K, Qr, Kr,
                                 (cudaStream_t)stream);
     return e == cudaSuccess ? HSA_OK : cuda_fail(e, "rope kernel launch");
 }
@@ -444,7 +445,7 @@ hsa_status_t hsa_paged_append(const hsa_paged_t *prob, const hsa_rope_t *rope, c
     HSA_TRY(shape_of(prob, &a));
     RopeArgs r;
     if (rope) HSA_TRY(rope_args(rope, a.d, &r));
-    HSA_TRY(check_head_count((Q ? a.H : 0) + 2 * a.Hkv));
+    HSA_TRY(check_head_count((Q ? a.H : 0) + 2ll * a.Hkv));
     const bool any = a.rows > 0 && a.B > 0;
     HSA_TRY(need(k_new, any, "k_new"));
     HSA_TRY(need(v_new, any, "v_new"));

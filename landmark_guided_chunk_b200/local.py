@@ -154,7 +154,7 @@ def rope(r: hsa_rope_t, Q=None, K=None, pos0: int = 0, pos=None, inverse: bool =
     H, Hkv = x.shape[2], K.shape[2] if K is not None else x.shape[2]
     if Q is not None and K is not None:
         _shape("K", K, (B, T, Hkv, d))
-        if H % Hkv:   # the heads are independent here: any two counts are fine, each in its own launch
+        if H + Hkv > 16383:   # the most that one launch takes
             return (rope(r, Q, None, pos0, pos, inverse, Q_out), rope(r, None, K, pos0, pos, inverse, None, K_out))
     if pos is not None:
         _ints(x, pos=pos)

@@ -174,6 +174,20 @@ def test_rope_call_refusals():
         hsa.make_rope(64, scaling="other")
 
 
+def test_rope_takes_any_two_head_counts():
+    """The rotation has no group: any H and Hkv, up to the heads of a launch (nothing is launched without rows)."""
+    L = _native.lib()
+    r = ctypes.byref(hsa.make_rope(64))
+    for H, Hkv in ((32, 1), (5, 2), (2, 7), (1, 1), (16000, 383)):
+        p = ctypes.byref(_window(H=H, Hkv=Hkv, Tq=0))
+        assert L.hsa_rope(r, p, None, 0, PTR, PTR, PTR, PTR, None) == 0, (H, Hkv)
+    top = 2 ** 31 - 1
+    for H, Hkv, status in ((16000, 384, UNSUPPORTED), (top, top, UNSUPPORTED), (top, 1, UNSUPPORTED), (0, 4, INVALID),
+                           (4, 0, INVALID), (-1, 4, INVALID)):
+        p = ctypes.byref(_window(H=H, Hkv=Hkv, Tq=3))
+        assert L.hsa_rope(r, p, None, 0, PTR, PTR, PTR, PTR, None) == status, (H, Hkv)
+
+
 def test_binding_refusals():
     x = torch.zeros(1, 4, 2, 64)
     for call in (lambda: hsa.window_attend(x, x, x, 3), lambda: hsa.rope(hsa.make_rope(64), x),

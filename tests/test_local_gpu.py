@@ -348,6 +348,17 @@ def test_rope_forms():
     check("rope", hsa.rope(r, big, pos0=9), want, tol)
 
 
+@pytest.mark.parametrize("H,Hkv", [(32, 1), (2, 7), (40, 2), (16380, 4)])
+def test_rope_head_counts(H, Hkv):
+    """Any two counts, more than 16 query heads to a kv head among them; above 16383 in all, in two launches."""
+    r = hsa.make_rope(32)
+    Q, K = _rand(1, BF, 2, 9, H, 64), _rand(2, BF, 2, 9, Hkv, 64)
+    pos = torch.arange(5, 14, device="cuda").expand(2, 9)
+    for x, y in zip((Q, K), hsa.rope(r, Q, K, pos0=5)):
+        want, tol = turn(x, pos, 32)
+        check("rope", y, want, tol)
+
+
 def test_rope_gradient_is_the_transpose():
     """<rope(x), g> = <x, rope_inverse(g)> in fp32, each side's sum off by its roundings."""
     r = hsa.make_rope(48, scaling="yarn", factor=8.0, orig_len=4096, interleaved=True)
