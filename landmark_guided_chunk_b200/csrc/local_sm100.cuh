@@ -65,7 +65,7 @@ struct PollLimit {
 // issued: the loader's own waits have the plain limit, and what it has issued is at most a ring away.
 __device__ __forceinline__ bool mbar_wait_ahead(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *status,
                                                 const volatile uint32_t *step) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity) || mbar_try_wait_suspend(bar, parity, SUSPEND_NS)) return true;
     uint32_t seen = *step;
     uint64_t t0 = globaltimer_ns();
     while (true) {
