@@ -24,6 +24,7 @@ struct LocArgs {
     int paged, page_shift, npages, max_pages;
     const int32_t *q_start, *kv_len, *table;
     int nsplit;            // key-axis splits per (sequence, kv head, row tile)
+    int by_rows;           // CUDA-core forward: row tiles numbered over all sequences (tile_by_row)
     float *opart, *lpart;  // split partials: [nsplit][rows][H][d] and [nsplit][rows][H] (tcgen05: by slot)
     long long *tc_starts;  // tcgen05: starts of the blocks' key tiles when CTAs take equal shares of them; else null
     float *lse;            // optional output
@@ -54,6 +55,21 @@ __device__ __forceinline__ Seq seq_of(const LocArgs &a, int b) {
     s.pos0 = s.kv - s.n;
     if (s.row0 != r0 || s.row0 + s.n != r1 || s.kv != kv) atomicOr(a.status, DEV_BAD_INDEX);
     return s;
+}
+
+// Row tiles of `tok` tokens numbered over all sequences: those of sequence b start at q_start[b] / tok + b, which leaves
+// each room enough (rounding down may leave one too many).  False: tile x has no tokens.
+__device__ __forceinline__ bool tile_by_row(const LocArgs &a, int x, int tok, int *b, int *blk) {
+    auto first = [&](int i) { return min(max(a.q_start[i], 0), a.rows) / tok + i; };
+    int lo = 0, hi = a.B - 1;   // the last b that starts at or before x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first(mid) <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    *b = lo;
+    *blk = x - first(lo);
+    return *blk >= 0;
 }
 
 // Row of the K/V tensors (in tokens) that holds token u of sequence b, or -1

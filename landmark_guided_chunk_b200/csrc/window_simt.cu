@@ -145,9 +145,11 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
     extern __shared__ __align__(16) float sm[];
     constexpr int BM = 16 * RM;   // rows (token, head) of this block
     float *sQ = sm, *sK = sQ + BM * D, *sV = sK + BN * (D + 4), *sP = sV + BN * D;
-    const int b = blockIdx.z, j = blockIdx.y;
-    const int split = blockIdx.x % a.nsplit, blk = blockIdx.x / a.nsplit;
+    const int j = blockIdx.y;
+    const int split = blockIdx.x % a.nsplit;
     const int tok = BM / a.G;                       // tokens per block
+    int b = blockIdx.z, blk = blockIdx.x / a.nsplit;
+    if (a.by_rows && !tile_by_row(a, blk, tok, &b, &blk)) return;
     const Seq s = seq_of(a, b);
     const int t0 = blk * tok, t1 = min(s.n, t0 + tok);
     if (t0 >= s.n) return;
@@ -497,13 +499,20 @@ template <typename F> cudaError_t with_smem(F f, size_t bytes) {
 }
 
 template <typename T, int D, int RM>
-cudaError_t fwd_rows(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
+cudaError_t fwd_rows(LocArgs a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
     constexpr int BM = 16 * RM;
     const size_t smem = (BM * D + BN * (D + 4) + BN * D + BM * PP) * sizeof(float);
     cudaError_t e = with_smem(simt_fwd_kernel<T, D, RM>, smem);
     if (e != cudaSuccess) return e;
     const int tok = BM / a.G;
-    const dim3 grid((unsigned)((a.max_q + tok - 1) / tok) * a.nsplit, a.Hkv, a.B);
+    dim3 grid((unsigned)((a.max_q + tok - 1) / tok) * a.nsplit, a.Hkv, a.B);
+    // max_q bounds the tokens of every paged sequence and may be far above most (all rows, if the caller knows no
+    // better): 65535 single tokens would get 2.7e8 blocks per kv head with it, minutes of empty ones.  Beyond 2^20
+    // blocks (about 5 ms of them) the tiles are numbered over the rows, a search in q_start per block.
+    if (a.paged && a.nsplit == 1 && (double)grid.x * a.Hkv * a.B > 1 << 20) {
+        a.by_rows = 1;
+        grid = dim3((unsigned)(a.rows / tok + a.B), a.Hkv, 1);
+    }
     simt_fwd_kernel<T, D, RM><<<grid, NT, smem, st>>>(a, (const T *)Q, (const T *)K, (const T *)V, (T *)O);
     return cudaGetLastError();
 }

@@ -22,6 +22,8 @@
 // window 4096: 3.83 ms, 1.11 PFLOP/s of visible pairs (66% of the measured 1.68); 16384
 // tokens: 0.90 ms; window 512: 0.226 ms (0.60 PFLOP/s: a fifth of its keys are masked and
 // an item's start and end cost four key tiles); head dim 64, window 4096: 0.83 ms.
+#include <limits.h>
+
 #include "local.cuh"
 #include "local_sm100.cuh"
 
@@ -117,7 +119,9 @@ __device__ __forceinline__ void block_of(const LocArgs &a, int g, int tok, int n
 // Which items a CTA takes.  Many items: every gridDim.x-th one.  Few: the key tiles of all items in a row, cut into
 // equal shares, one per CTA (lengths differ, and whole items would leave most SMs waiting for the longest); an item
 // that a cut goes through is written as partials and joined by join_kernel.
-struct Walk {
+// LOOSE steps over a sequence's blocks without tokens, which come first: for paged calls whose max_q is far above most
+// sequences' tokens (launch_tc).
+template <bool LOOSE> struct Walk {
     Share s;             // shares: what is left; else s.g: the next item
     bool first;
     __device__ __forceinline__ bool next(const LocArgs &a, bool shares, int tok, int nblk, int nitems, Item *it) {
@@ -128,6 +132,10 @@ struct Walk {
             it->i0 = 0;
             it->i1 = it->tl.nt;
             it->slot = -1;
+            if (LOOSE && it->ntile == 0) {   // past this item and the others
+                const int first = (it->b * nblk + nblk - (it->s.n + 2 * tok - 1) / (2 * tok)) * a.Hkv;
+                s.g += (first - s.g - 1) / (int)gridDim.x * (int)gridDim.x;
+            }
             s.g += gridDim.x;
             return true;
         }
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <int D>
+template <int D, bool LOOSE>
 __global__ void __launch_bounds__(NT, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(NT, 1)
         uint32_t n = 0, na = 0;                  // tiles of S, items with keys so far
         bool ok = true;
         Item it;
-        for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
+        for (Walk<LOOSE> walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
             const bool any = it.i1 > it.i0;
             if (t >= it.ntile) {
                 na += any;
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t qused = 0;                  // bit 2 x + t: filled before
             bool ok = true;
             Item it;
-            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
+            for (Walk<LOOSE> walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 for (int i = it.i0; i < it.i1 && ok; ++i) {
                     const int u0 = it.tl.start(i);
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t qpar = 0, p_par = 0, kvpar = 0, na = 0, head = 0;   // bits: parities of the next phases
             bool ok = true;
             Item it;
-            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
+            for (Walk<LOOSE> walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 const int nt = it.i1 - it.i0, x = na++ % C::QB;   // key tiles, Q buffer
                 // ring stages of K and V of tile i and of K of tile i + 1
@@ -668,7 +676,7 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t na = 0, par = 0;
             bool ok = true;
             Item it;
-            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
+            for (Walk<LOOSE> walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 const int x = na++ % C::QB;
                 for (int t = 0; t < it.ntile; ++t) {
@@ -693,7 +701,7 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t nkv = 0, land_par = 0;
             bool ok = true;
             Item it;
-            for (Walk walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
+            for (Walk<LOOSE> walk{bar->share, true}; ok && walk.next(a, shares, tok, nblk, nitems, &it);) {
                 if (it.ntile == 0 || it.i0 >= it.i1) continue;
                 for (int i = it.i0; i < it.i1 && ok; ++i, nkv += 2) {
                     if (!it.tl.has_dead(i)) continue;
@@ -725,7 +733,10 @@ __global__ void __launch_bounds__(NT, 1)
 }  // namespace
 
 bool tc_supported(const LocArgs &a, int dtype) {
-    return dtype == HSA_BF16 && a.max_kv > 0 && a.max_q > 0;
+    if (dtype != HSA_BF16 || a.max_kv == 0 || a.max_q == 0) return false;
+    // items are numbered in 32 bits, with room for a step past the last (a loose max_q of very many sequences)
+    const int tok = MR / a.G, nblk = (a.max_q + 2 * tok - 1) / (2 * tok);
+    return (long long)a.B * nblk * a.Hkv <= INT_MAX - 148;
 }
 
 cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st) {
@@ -753,8 +764,16 @@ cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void
         kern<<<grid, NT, smem, st>>>(mq, mk, mv, mo, (__nv_bfloat16 *)O, a, tok, nblk, (int)items, starts);
         return cudaGetLastError();
     };
-    e = a.d == 64 ? go(window_fwd_kernel<64>, Cfg<64>::TILE, 2 * Cfg<64>::QB + Cfg<64>::NST)
-                  : go(window_fwd_kernel<128>, Cfg<128>::TILE, 2 * Cfg<128>::QB + Cfg<128>::NST);
+    // Far more items than the rows can fill: the walk that steps over the empty ones.  It makes an item's start longer
+    // (300 items of 6 key tiles: 35.2 -> 36.9 us), so only where they are most.  20000 single tokens: max_q 20399
+    // (318 blocks each) 40.6 -> 13.9 ms, max_q 300 (5 blocks) 1.45 -> 1.73 ms.
+    const bool loose = a.paged && (long long)a.B * nblk > 16 * (a.rows / (2ll * tok) + a.B);
+    auto by_walk = [&](auto kern, auto kern_loose, int tile, int tiles) {
+        return loose ? go(kern_loose, tile, tiles) : go(kern, tile, tiles);
+    };
+    e = a.d == 64 ? by_walk(window_fwd_kernel<64, false>, window_fwd_kernel<64, true>, Cfg<64>::TILE, 2 * Cfg<64>::QB + Cfg<64>::NST)
+                  : by_walk(window_fwd_kernel<128, false>, window_fwd_kernel<128, true>, Cfg<128>::TILE,
+                            2 * Cfg<128>::QB + Cfg<128>::NST);
     if (e != cudaSuccess || !starts) return e;
     const dim3 jg((unsigned)items, 2 * JOIN_ROWS);
     if (a.d == 64) window_join_kernel<64><<<jg, 256, 0, st>>>(a, (__nv_bfloat16 *)O, tok, nblk, starts);

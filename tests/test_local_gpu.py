@@ -464,6 +464,48 @@ def test_paged_few_sequences(dt, new, kv):
     _paged(dt, 128, 4, 2, new, kv, 16, 50, 2)
 
 
+def _loose(dt, d, H, Hkv, new, kv, sample, **kw):
+    """paged_attend without max_q: every sequence may hold all rows, as far as the call knows."""
+    B, page = len(new), 16
+    need = torch.tensor([-(-m // page) for m in kv])
+    table = torch.full((B, int(need.max())), -1, dtype=torch.int32)
+    at = torch.cat((torch.zeros(1, dtype=torch.long), need.cumsum(0)))
+    for i in range(table.shape[1]):
+        table[need > i, i] = (at[:-1][need > i] + i).to(torch.int32)
+    q_start = torch.cat((torch.zeros(1, dtype=torch.long), torch.tensor(new).cumsum(0)))
+    rows = int(q_start[-1])
+    Q, K, V = _rand(1, dt, rows + 2, H, d), _rand(2, dt, int(at[-1]), page, Hkv, d), _rand(3, dt, int(at[-1]), page, Hkv, d)
+    args = [x.to(torch.int32).cuda() for x in (q_start, torch.tensor(kv), table)]
+    ws = hsa.paged_workspace(Q, K, args[2], **kw)
+    O = torch.full_like(Q, 7.0)
+    hsa.paged_attend(Q, K, V, *args, O=O, ws=ws, **kw)
+    _clean(ws)
+    assert bool((O[rows:] == 7.0).all())
+    for b in sample:
+        r0, m = int(q_start[b]), kv[b]
+        k, v = (X[int(at[b]):int(at[b + 1])].reshape(-1, Hkv, d)[:m] for X in (K, V))
+        if new[b]:
+            r = Ref(Q[r0:r0 + new[b]], k, v, torch.arange(m - new[b], m, device="cuda"), m, 0, 0)
+            check(f"O[{b}]", O[r0:r0 + new[b]], r.O, r.tO)
+    return O[:rows]
+
+
+@pytest.mark.parametrize("dt,simt", [(BF, False), (BF, True), (F32, False)])
+def test_paged_many_sequences_without_a_bound(dt, simt):
+    """20000 sequences of a token each, a few longer or empty: blocks without tokens by the million."""
+    new, kv = [1] * 20000, [1 + i % 20 for i in range(20000)]
+    for b, n in ((7, 300), (8, 0), (9, 0), (5000, 33), (19998, 0), (19999, 65)):
+        new[b], kv[b] = n, n + 9
+    O = _loose(dt, 64, 8, 2, new, kv, [0, 1, 6, 7, 10, 11, 4999, 5000, 5001, 13000, 19997, 19999], force_simt=simt)
+    assert not bool((O == 7.0).flatten(1).all(1).any())
+
+
+def test_paged_items_beyond_32_bits():
+    """65535 sequences that may hold 65535 rows each, over 9 kv heads of 16: 2.4e9 pairs of row tiles."""
+    O = _loose(BF, 64, 144, 9, [1] * 65535, [1 + i % 5 for i in range(65535)], [0, 1, 2, 30000, 65533, 65534])
+    assert not bool((O == 7.0).flatten(1).all(1).any())
+
+
 def test_paged_bad_pages_and_lengths():
     """Page numbers outside the pool read as zeros and lengths are cut to their bounds; both are reported."""
     P = Pages(BF, 64, 4, 2, [4, 1], [100, 40], 32)

@@ -233,3 +233,49 @@ def test_a_producer_that_gives_up_waits_for_its_loads(nst):
     # parity 0 for every stage passes with the second use still in flight, and waits on stages without a load
     zero = lambda issued, x, nst: 0    # noqa: E731
     assert _drained(2 * nst, nst, nst, zero) and not _drained(1, 1, nst, zero)
+
+
+def _tile_by_row(q_start, x, tok):
+    """tile_by_row of csrc/local.cuh: (sequence, its block) of the x-th row tile over all sequences, or None."""
+    first = lambda i: q_start[i] // tok + i    # noqa: E731
+    lo, hi = 0, len(q_start) - 2
+    while lo < hi:
+        mid = (lo + hi + 1) >> 1
+        lo, hi = (mid, hi) if first(mid) <= x else (lo, mid - 1)
+    return (lo, x - first(lo)) if x >= first(lo) else None
+
+
+def _ragged(rng):
+    n = [rng.choice([0, 1, 1, 1, 2, 7, 300]) for _ in range(rng.randint(1, 40))]
+    return n, [sum(n[:i]) for i in range(len(n) + 1)]
+
+
+@pytest.mark.parametrize("tok", [1, 4, 5, 32])
+def test_row_tiles_over_all_sequences_cover_each_block_once(tok):
+    for seed in range(100):
+        n, q_start = _ragged(random.Random(seed))
+        got = [_tile_by_row(q_start, x, tok) for x in range(q_start[-1] // tok + len(n))]
+        live = [g for g in got if g and g[1] * tok < n[g[0]]]
+        assert sorted(live) == [(b, k) for b, m in enumerate(n) for k in range(-(-m // tok))]
+
+
+@pytest.mark.parametrize("grid,hkv,tok", [(148, 2, 4), (148, 8, 32), (5, 3, 1)])
+def test_the_walk_past_empty_blocks_meets_every_item(grid, hkv, tok):
+    """Walk::next of csrc/window_tc.cu: a sequence's blocks without tokens come first and are stepped over."""
+    for seed in range(60):
+        n, q_start = _ragged(random.Random(seed))
+        nblk = -(-q_start[-1] // (2 * tok))
+        blocks = [-(-m // (2 * tok)) for m in n]
+        want = [g for g in range(len(n) * nblk * hkv) if nblk - 1 - g // hkv % nblk < blocks[g // hkv // nblk]]
+        got, looks = [], 0
+        for g in range(grid):
+            while g < len(n) * nblk * hkv:
+                b, on = g // hkv // nblk, 1
+                looks += 1
+                if nblk - 1 - g // hkv % nblk < blocks[b]:
+                    got.append(g)
+                else:
+                    on += ((b * nblk + nblk - blocks[b]) * hkv - g - 1) // grid
+                    assert on >= 1
+                g += on * grid
+        assert sorted(got) == want and looks <= len(want) + len(n) * grid
