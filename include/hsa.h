@@ -380,6 +380,8 @@ typedef struct {
  * of sum_u exp(scale q . K[u]), -inf where no key is visible; hsa_window_backward needs it.
  * bf16 rounds the probabilities to bf16 before the product with V (fp32 sums); fp32 and HSA_FLAG_SIMT
  * keep fp32 throughout.  The sums' order depends on the sizes only: equal calls give equal bits.
+ * A workspace of the size returned also serves every call with a smaller B, Tq or Tkv and the other
+ * fields equal (q_pos0 and kv_cap may differ).
  */
 HSA_API hsa_status_t hsa_window_workspace_size(const hsa_window_t *p, size_t *bytes);
 HSA_API hsa_status_t hsa_window_attend(const hsa_window_t *p, const void *Q, const void *K, const void *V, void *O,
@@ -393,6 +395,8 @@ HSA_API hsa_status_t hsa_window_attend(const hsa_window_t *p, const void *Q, con
  * [B][Tcap][Hkv][d] (zeros for tokens that no query sees).  O and lse as hsa_window_attend returned
  * them.  bf16 rounds P and dS to bf16 before their products; where a row sees few keys (up to 64), D is
  * sum P (dO . v) in fp32, without the rounding of the bf16 O.  No atomics: equal calls give equal bits.
+ * The workspace size is that of this problem alone: a smaller one, whose rows are shared between more
+ * blocks, may need more.
  */
 HSA_API hsa_status_t hsa_window_backward_workspace_size(const hsa_window_t *p, size_t *bytes);
 HSA_API hsa_status_t hsa_window_backward(const hsa_window_t *p, const void *Q, const void *K, const void *V,
@@ -478,7 +482,9 @@ HSA_API hsa_status_t hsa_paged_append(const hsa_paged_t *p, const hsa_rope_t *ro
  * with the visibility above.  Q, O [rows][H][d].  Pages wholly behind every query's window are never
  * read: their table entries may be stale.  A page number outside [0, npages) where a key is visible
  * reads as zero keys and values, and a length outside its bounds is cut to them; both are recorded in
- * the status word (HSA_ERR_INVALID_ARG).
+ * the status word (HSA_ERR_INVALID_ARG).  A workspace of the size returned also serves every call with
+ * a smaller B, rows, max_q or max_kv (as they are after their defaults) and the other fields equal
+ * (npages and max_pages may differ), and hsa_paged_append.
  */
 HSA_API hsa_status_t hsa_paged_workspace_size(const hsa_paged_t *p, size_t *bytes);
 HSA_API hsa_status_t hsa_paged_attend(const hsa_paged_t *p, const void *Q, const void *Kp, const void *Vp,

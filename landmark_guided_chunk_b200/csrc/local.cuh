@@ -25,7 +25,7 @@ struct LocArgs {
     const int32_t *q_start, *kv_len, *table;
     int nsplit;            // key-axis splits per (sequence, kv head, row tile)
     int by_rows;           // CUDA-core forward: row tiles numbered over all sequences (tile_by_row)
-    float *opart, *lpart;  // split partials: [nsplit][rows][H][d] and [nsplit][rows][H] (tcgen05: by slot)
+    float *opart, *lpart;  // split partials: [nsplit][B][max_q][H][d] and [nsplit][B][max_q][H] (tcgen05: by slot)
     long long *tc_starts;  // tcgen05: starts of the blocks' key tiles when CTAs take equal shares of them; else null
     float *lse;            // optional output
     uint32_t *status;
@@ -83,6 +83,12 @@ __device__ __forceinline__ long long kv_row(const LocArgs &a, int b, int u) {
         return -1;
     }
     return ((long long)pg << a.page_shift) + (u & ((1 << a.page_shift) - 1));
+}
+
+// First row of the split partials of token t of sequence b (one row per head).  Numbered by sequence, not by row of Q:
+// rows behind the last sequence, of which there may be any number, have none.
+__device__ __forceinline__ long long part_row(const LocArgs &a, int split, int b, int t) {
+    return (((long long)split * a.B + b) * a.max_q + t) * a.H;
 }
 
 __host__ __device__ __forceinline__ bool visible(int p, int u, int kv, int window, int sinks) {
@@ -180,7 +186,8 @@ __host__ __device__ __forceinline__ KvRange kv_range(const BwdArgs &w, const Seq
 struct LocPlan {
     bool tc, few;          // forward path: tcgen05 tiles, few-row kernel; neither: CUDA-core tiles
     int nsplit;
-    size_t opart, lpart, starts, total;   // offsets; starts 0: no shares
+    size_t opart, lpart, starts;   // offsets; starts 0: no shares
+    size_t total;                  // enough for every call of smaller B, rows, max_q and max_kv too
 };
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt);
 
@@ -203,6 +210,7 @@ struct TcPlan {
     size_t starts, opart, lpart;    // bytes
 };
 TcPlan tc_plan(const LocArgs &a, long long most_keys);   // most_keys: that one block can see
+TcPlan tc_plan_most(const LocArgs &a, long long most_keys);   // the most that tc_plan of a smaller call can need
 cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void *V, void *O, cudaStream_t st);
 cudaError_t launch_combine(const LocArgs &a, int dtype, void *O, cudaStream_t st);
 cudaError_t launch_rowdot(const LocArgs &a, int dtype, const void *O, const void *dO, float *D, cudaStream_t st);

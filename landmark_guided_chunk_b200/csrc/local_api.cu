@@ -142,6 +142,33 @@ long long most_keys(const LocArgs &a, int tok) {
     return w < a.max_kv ? w : a.max_kv;
 }
 
+// The most bytes beyond the header that plan_forward of a call with a smaller (or equal) B, rows, max_q and max_kv can
+// need, so that one workspace serves a server's batches of any size up to its largest.  Smaller calls are split
+// more: below, items are work items, and a call of n of them gets at most 2 SMS / n splits.
+static size_t forward_most(const LocArgs &a, int dtype, bool simt) {
+    if (a.B == 0 || a.max_q == 0 || a.max_kv == 0) return 0;
+    auto partials = [&](long long rows) {   // rows: of all heads and splits
+        return rows > 0 ? align256((size_t)rows * a.d * sizeof(float)) + align256((size_t)rows * sizeof(float)) : 0;
+    };
+    auto least = [](long long x, long long y) { return x < y ? x : y; };
+    const long long rows = (long long)a.max_q * a.G, heads = (long long)a.B * a.Hkv;
+    if (simt || dtype != HSA_BF16) {
+        // items of up to 32 rows (64 only where they fill the SMs unsplit), two key tiles per split at least
+        const long long block = rows <= 16 ? 16 : 32, nt = ceil_div(most_keys(a, (int)(block / a.G)), 64) + 1;
+        return nt / 2 < 2 || a.Hkv > SMS ? 0 : partials(least(2 * SMS * block, heads * rows * least(64, nt / 2)));
+    }
+    // few rows: partials beyond a cluster's splits
+    const int tok = (int)least(a.max_q, 16 / a.G);
+    const bool few = ceil_div(most_keys(a, tok), 64) + 1 >= 32 * FEW_CLUSTER && a.Hkv * FEW_CLUSTER < SMS;
+    size_t most = few ? partials((long long)tok * a.G * least(2 * SMS, 64 * heads)) : 0;
+    if (rows > 16) {
+        const TcPlan t = tc_plan_most(a, most_keys(a, 2 * (128 / a.G)));
+        const size_t n = align256(t.starts) + align256(t.opart) + align256(t.lpart);
+        if (n > most) most = n;
+    }
+    return most;
+}
+
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
     LocPlan p{};
     p.nsplit = 1;
@@ -182,12 +209,13 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
             off += align256(t.lpart);
         }
     } else if (p.nsplit > (p.few ? FEW_CLUSTER : 1)) {
-        const size_t r = (size_t)a.rows * a.H * p.nsplit;
+        const size_t r = (size_t)a.B * a.max_q * a.H * p.nsplit;
         off += align256(r * a.d * sizeof(float));
         p.lpart = off;
         off += align256(r * sizeof(float));
     }
-    p.total = off;
+    const size_t most = HDR + forward_most(a, dtype, simt);
+    p.total = off > most ? off : most;
     return p;
 }
 

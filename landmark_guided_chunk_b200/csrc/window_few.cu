@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(NT) window_few_kernel(const __grid_constant__ 
         const float lse = l > 0.f ? mx * 0.6931471805599453f + logf(l) : -INFINITY;
         const long long row = (long long)(s.row0 + r / a.G) * a.H + j * a.G + r % a.G;
         if (!CLUSTER && a.nsplit > 1) {
-            const long long prow = (long long)split * a.rows * a.H + row;
+            const long long prow = part_row(a, split, b, r / a.G) + j * a.G + r % a.G;
             *reinterpret_cast<float4 *>(a.opart + prow * D + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             if (c == 0) a.lpart[prow] = lse;
         } else {

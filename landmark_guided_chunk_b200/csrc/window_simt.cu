@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(NT) simt_fwd_kernel(LocArgs a, const T *__rest
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         const float lse = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
         const long long row = (long long)(s.row0 + t0 + r / a.G) * a.H + j * a.G + r % a.G;
-        const long long prow = (long long)split * a.rows * a.H + row;
+        const long long prow = part_row(a, split, b, t0 + r / a.G) + j * a.G + r % a.G;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
             float x, y, z, w;
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(256) combine_kernel(LocArgs a, T *__restrict__
     const long long e = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (e >= (long long)s.n * a.H) return;
     const long long row = (long long)s.row0 * a.H + e;
-    const long long stride = (long long)a.rows * a.H;
+    const long long prow = part_row(a, 0, b, 0) + e, stride = part_row(a, 1, 0, 0);
     float mx = -INFINITY;
-    for (int i = lane; i < a.nsplit; i += 32) mx = fmaxf(mx, a.lpart[i * stride + row]);
+    for (int i = lane; i < a.nsplit; i += 32) mx = fmaxf(mx, a.lpart[i * stride + prow]);
     mx = warp_max(mx);
     constexpr int N = D / 32;
     float acc[N], l = 0.f;
@@ -263,9 +263,9 @@ __global__ void __launch_bounds__(256) combine_kernel(LocArgs a, T *__restrict__
     for (int x = 0; x < N; ++x) acc[x] = 0.f;
     if (mx != -INFINITY) {
         for (int i = 0; i < a.nsplit; ++i) {
-            const float w = expf(a.lpart[i * stride + row] - mx);
+            const float w = expf(a.lpart[i * stride + prow] - mx);
             l += w;
-            const float *src = a.opart + (i * stride + row) * D + lane * N;
+            const float *src = a.opart + (i * stride + prow) * D + lane * N;
 #pragma unroll
             for (int x = 0; x < N; ++x) acc[x] = fmaf(w, src[x], acc[x]);
         }

@@ -781,6 +781,18 @@ cudaError_t launch_tc(const LocArgs &a, const void *Q, const void *K, const void
     return cudaGetLastError();
 }
 
+static int share_items(const LocArgs &a) { return (a.paged ? 16 : 2) * 148; }   // fewer items than these are shared
+constexpr long long SHARE_BLOCKS = 1024;
+
+static void share_bytes(const LocArgs &a, long long blocks, long long items, long long most_keys, TcPlan *p) {
+    p->starts = (size_t)(blocks + 2) * sizeof(long long);
+    // two slots (first and last item) for each CTA that can get a share
+    long long ctas = items * (most_keys / BK + 3) / SHARE_LEAST + 1;
+    if (ctas > 148) ctas = 148;
+    p->opart = (size_t)(2 * ctas) * 2 * MR * a.d * sizeof(float);
+    p->lpart = (size_t)(2 * ctas) * 2 * MR * sizeof(float);
+}
+
 TcPlan tc_plan(const LocArgs &a, long long most_keys) {
     const int tok = MR / a.G, nblk = (a.max_q + 2 * tok - 1) / (2 * tok);
     const long long blocks = (long long)a.B * nblk, items = blocks * a.Hkv;
@@ -790,15 +802,18 @@ TcPlan tc_plan(const LocArgs &a, long long most_keys) {
     // keys (2048 items of 33 tiles: 890 us whole, 1148 us shared); items of fewer than 16 key tiles are not worth
     // their cuts and the second launch (300 of 6 tiles: 35 us whole, 53 us and the join shared; but 136 of 113 to 256: 833 us and 492 us).
     // The scan of the blocks' lengths, one warp per CTA, is kept to 1024 blocks.
-    p.shares = items > 0 && items < (a.paged ? 16 : 2) * 148 && blocks <= 1024 && most_keys >= 16 * BK;
-    if (p.shares) {
-        p.starts = (size_t)(blocks + 2) * sizeof(long long);
-        // two slots (first and last item) for each CTA that can get a share
-        long long ctas = items * (most_keys / BK + 3) / SHARE_LEAST + 1;
-        if (ctas > 148) ctas = 148;
-        p.opart = (size_t)(2 * ctas) * 2 * MR * a.d * sizeof(float);
-        p.lpart = (size_t)(2 * ctas) * 2 * MR * sizeof(float);
-    }
+    p.shares = items > 0 && items < share_items(a) && blocks <= SHARE_BLOCKS && most_keys >= 16 * BK;
+    if (p.shares) share_bytes(a, blocks, items, most_keys, &p);
+    return p;
+}
+
+TcPlan tc_plan_most(const LocArgs &a, long long most_keys) {
+    const int tok = MR / a.G, nblk = (a.max_q + 2 * tok - 1) / (2 * tok);
+    const long long blocks = (long long)a.B * nblk, items = blocks * a.Hkv;
+    TcPlan p{};
+    p.shares = items > 0 && a.Hkv < share_items(a) && most_keys >= 16 * BK;
+    if (p.shares)
+        share_bytes(a, blocks < SHARE_BLOCKS ? blocks : SHARE_BLOCKS, items < share_items(a) ? items : share_items(a), most_keys, &p);
     return p;
 }
 

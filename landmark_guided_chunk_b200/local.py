@@ -190,7 +190,8 @@ def _window(Q, K, window, sinks, q_pos0, kv_len, scale, force_simt):
 
 
 def window_workspace(Q, K, window, sinks=0, q_pos0=0, kv_len=None, backward=False, force_simt=False) -> torch.Tensor:
-    """A workspace for window_attend on these shapes (backward: for window_backward too)."""
+    """A workspace for window_attend on these shapes and on every smaller batch or length.  backward: for
+    window_backward too, on these shapes alone."""
     prob = _window(Q, K, window, sinks, q_pos0, kv_len, 0.0, force_simt)
     ws = _workspace("hsa_window_workspace_size", prob, Q.device)
     if backward:
@@ -249,7 +250,8 @@ def _paged(H, rows, Kp, table, max_q, max_kv, window, sinks, scale, force_simt):
 
 
 def paged_workspace(Q, K_pages, table, max_q=None, max_kv=0, window=0, sinks=0, force_simt=False) -> torch.Tensor:
-    """A workspace for paged_append and paged_attend on these shapes and bounds."""
+    """A workspace for paged_append and paged_attend on these shapes and bounds and on all smaller ones: a server's
+    largest batch's serves the others (one call at a time)."""
     prob = _paged(Q.shape[1], Q.shape[0], K_pages, table, Q.shape[0] if max_q is None else max_q, max_kv, window,
                   sinks, 0.0, force_simt)
     return _workspace("hsa_paged_workspace_size", prob, Q.device)

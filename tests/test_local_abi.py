@@ -3,6 +3,7 @@ entry points (an invalid call launches nothing, so no GPU is needed)."""
 import ctypes
 import math
 import os
+import random
 import subprocess
 import sys
 
@@ -83,6 +84,45 @@ def test_positions_up_to_the_last_64_bit_one_are_refused(q_pos0):
     r = hsa.make_rope(64)
     assert L.hsa_rope(ctypes.byref(r), p, None, 0, PTR, PTR, PTR, PTR, None) == UNSUPPORTED
     assert L.hsa_window_workspace_size(ctypes.byref(_window(q_pos0=(1 << 30) - 100)), ctypes.byref(n)) == 0
+
+
+def _bytes(prob):
+    n = ctypes.c_size_t()
+    f = _native.lib().hsa_paged_workspace_size if isinstance(prob, hsa_paged_t) else _native.lib().hsa_window_workspace_size
+    assert f(ctypes.byref(prob), ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("dtype,flags", [(1, 0), (0, 0), (1, _native.HSA_FLAG_SIMT)])
+def test_a_workspace_serves_every_smaller_batch(dtype, flags):
+    """A server sizes its workspace for the largest batch; smaller ones, which are split more, must fit it."""
+    rng = random.Random(1)
+
+    def size(hi):
+        return min(hi, int(2 ** rng.uniform(0, math.log2(hi + 1))))
+
+    partials = 0
+    for _ in range(4000):
+        Hkv, G, d = rng.choice([1, 2, 3, 8, 19, 32, 150, 300]), rng.choice([1, 3, 4, 5, 8, 16]), rng.choice([64, 128])
+        win = rng.choice([0, 0, 100, 5000])
+        same = dict(H=Hkv * G, Hkv=Hkv, d=d, dtype=dtype, flags=flags, window=win, sinks=rng.choice([0, 4, 3000]) if win else 0)
+        big = dict(B=size(80), max_q=size(20000), max_kv=size(1 << 22))
+        big["rows"] = big["max_q"] + size(100000)
+        small = {k: rng.choice([v, size(v)]) for k, v in big.items()}
+        paged = [_bytes(_paged(max_pages=1 << 19, **same, **x)) for x in (big, small)]
+        window = [_bytes(_window(B=x["B"], Tq=x["max_q"], Tkv=x["max_kv"], q_pos0=0, **same)) for x in (big, small)]
+        assert paged[1] <= paged[0], (same, big, small)
+        assert window[1] <= window[0], (same, big, small)
+        assert max(paged + window) < 64 << 20      # 148 CTAs' partials of two row tiles, or 296 blocks of 32 rows
+        partials += paged[1] > 256
+    assert partials > 400
+
+
+def test_workspaces_of_batches_of_a_server():
+    """32 + 8 heads of 128, pages of 64, up to 32768 keys: 32 sequences of up to 2048 new tokens down to single ones."""
+    same = dict(H=32, Hkv=8, d=128, page=64, npages=20000, max_pages=512, max_kv=32768)
+    n = [_bytes(_paged(B=B, rows=B * q, max_q=q, **same)) for B, q in ((32, 2048), (32, 512), (8, 512), (8, 1), (1, 1))]
+    assert n == sorted(n, reverse=True)
 
 
 def _each(fn, args, optional=()):

@@ -464,6 +464,27 @@ def test_paged_few_sequences(dt, new, kv):
     _paged(dt, 128, 4, 2, new, kv, 16, 50, 2)
 
 
+@pytest.mark.parametrize("dt,simt", [(BF, False), (BF, True), (F32, False)])
+def test_paged_one_workspace_for_every_batch(dt, simt):
+    """The workspace of the largest batch serves smaller ones, which are split more, one after another; rows behind the
+    last sequence, more of them than the batch has, take no part."""
+    d, H, Hkv, page = 64, 8, 2, 64
+    big = Pages(dt, d, H, Hkv, [300] * 6, [20000] * 6, page)
+    ws = hsa.paged_workspace(big.Q, big.K, big.table, max_q=300, max_kv=20000, force_simt=simt)
+    ws[256:] = 0xFF
+    for new, kv in (([300] * 6, [20000, 19000, 700, 301, 20000, 300]), ([1] * 6, [20000] * 6), ([1], [20000]), ([4], [17000]),
+                    ([200, 1], [20000, 20000]), ([2, 0, 1], [16500, 9, 20000]), ([40], [4000])):
+        P = Pages(dt, d, H, Hkv, new, kv, page, pad=400)
+        O = torch.full_like(P.Q, 7.0)
+        hsa.paged_attend(P.Q, P.K, P.V, P.q_start, P.kv_len, P.table, max_q=max(new), max_kv=max(kv), O=O, ws=ws, force_simt=simt)
+        _clean(ws)
+        for b in range(len(new)):
+            if new[b]:
+                r = Ref(P.Q[P.rows(b)], P.cache(b, P.K), P.cache(b, P.V), P.pos(b), kv[b], 0, 0)
+                check(f"O[{b}]", O[P.rows(b)], r.O, r.tO)
+        assert bool((O[sum(new):] == 7.0).all())
+
+
 def _loose(dt, d, H, Hkv, new, kv, sample, **kw):
     """paged_attend without max_q: every sequence may hold all rows, as far as the call knows."""
     B, page = len(new), 16
