@@ -123,12 +123,6 @@ template <int BK> __host__ __device__ __forceinline__ Tiles tiles_of(int pa, int
 // (Others are loaded as zeros: nothing of theirs reaches a sum, NaN included.)
 __host__ __device__ __forceinline__ bool key_live(const Tiles &t, int u) { return u < t.hi && (u >= t.lo || u < t.ns); }
 
-// True if every query at pa .. pb sees every key u0 .. u0 + n - 1 (no mask needed).
-__host__ __device__ __forceinline__ bool tile_full(int pa, int pb, int u0, int n, int kv, int window, int sinks) {
-    const int ul = u0 + n - 1;
-    return ul <= pa && ul < kv && (pb - u0 < window || ul < sinks);
-}
-
 // Split s of the nt tiles: [i0, i1).
 __host__ __device__ __forceinline__ void split_range(int nt, int nsplit, int s, int *i0, int *i1) {
     const int per = (nt + nsplit - 1) / nsplit;
@@ -194,7 +188,7 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt);
 struct BwdPlan {
     bool tc;
     int nkt, nwin, win_q, nst, nfar, far_q, npt, bk;
-    size_t D, part, extra, total;
+    size_t D, part, total;
 };
 BwdPlan plan_backward(const LocArgs &a, int dtype, bool simt);
 
