@@ -266,6 +266,8 @@ def paged_append(k_new, v_new, K_pages, V_pages, q_start, kv_len, table, Q=None,
     _check(k_new, v_new, K_pages, V_pages, Q, Q_out)
     _ints(k_new, q_start=q_start, kv_len=kv_len, table=table)
     rows, Hkv, d = k_new.shape
+    if Q is None and Q_out is not None:
+        raise ValueError("Q_out without Q")
     npages, page, B = K_pages.shape[0], K_pages.shape[1], table.shape[0]
     _shape("v_new", v_new, k_new.shape)
     _shape("K_pages", K_pages, (npages, page, Hkv, d))

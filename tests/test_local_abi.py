@@ -316,6 +316,16 @@ def test_binding_integers_at_the_ends_of_their_fields(calls):
             hsa.make_rope(**kw)
 
 
+def test_binding_refuses_an_output_without_its_input(calls):
+    x, i = _tensors()
+    with pytest.raises(ValueError, match="Q_out"):
+        hsa.paged_append(x[0], x[0], x, x, i[:2], i[:1], i[None], Q_out=x[0])
+    for kw in (dict(Q=x, K_out=x), dict(K=x, Q_out=x)):
+        with pytest.raises(ValueError, match="_out"):
+            hsa.rope(hsa.make_rope(64), **kw)
+    assert not calls
+
+
 @pytest.mark.parametrize("ws", [torch.zeros(1 << 20, dtype=torch.uint8),
                                 torch.zeros(1 << 21, dtype=torch.uint8)[::2].as_subclass(_OnDevice)], ids=["cpu", "strided"])
 def test_binding_workspaces(calls, ws):
