@@ -199,6 +199,35 @@ def test_window_backward_many_items(B):
     _backward(BF, 128, 8, 8, B, 150, 150, 150, 0, 0, 0)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_window_backward_far_rows(dt):
+    """Gradients of a cache of 2.3 G elements, 2^31 bytes and more per sequence: those of the window's and the sinks'
+    tokens, and zeros in between and behind the cached ones."""
+    B, cap, Hkv, d, w, S, Tq = 2, 1_100_000, 8, 128, 300, 5, 150
+    K = torch.empty(B, cap, Hkv, d, dtype=dt, device="cuda")
+    V, dK, dV = torch.empty_like(K), torch.empty_like(K), torch.empty_like(K)
+    assert K.numel() > 2 ** 31 and K[0].numel() * K.element_size() > 2 ** 31
+    n = cap - 7
+    cut = n - Tq - w - 16
+    for i, x in enumerate((K, V)):
+        x[:, cut:], x[:, :8] = _rand(i, dt, B, cap - cut, Hkv, d), _rand(i + 2, dt, B, 8, Hkv, d)
+    dK.fill_(math.nan)
+    dV.fill_(math.nan)
+    Q, dO = _rand(5, dt, B, Tq, 16, d), _rand(6, dt, B, Tq, 16, d)
+    kw = dict(q_pos0=n - Tq, kv_len=n)
+    O, lse = hsa.window_attend(Q, K, V, w, S, return_lse=True, **kw)
+    dQ, _, _ = hsa.window_backward(Q, K, V, O, lse, dO, w, S, out=(torch.empty_like(Q), dK, dV), **kw)
+    p = torch.arange(n - Tq, n, device="cuda") - cut + S
+    for b in range(B):
+        Ks, Vs = (torch.cat((x[b, :S], x[b, cut:n])) for x in (K, V))
+        r = Ref(Q[b], Ks, Vs, p, Ks.shape[0], w, S, None, dO[b])
+        check("dQ", dQ[b], r.dQ, r.tdQ)
+        for x, want, tol in ((dK, r.dK, r.tdK), (dV, r.dV, r.tdV)):
+            check("sinks", x[b, :S], want[:S], tol[:S])
+            check("window", x[b, cut:n], want[S:], tol[S:])
+            assert not bool(x[b, n:].any()) and not any(bool(y.any()) for y in x[b, S:cut].split(1 << 18))
+
+
 @pytest.mark.parametrize("d,H,Hkv,T,Tkv,pos0,window,sinks,simt", [
     (64, 4, 2, 70, 70, 0, 1, 0, False), (128, 8, 2, 100, 100, 0, 1, 1, False), (128, 3, 1, 45, 45, 0, 0, 0, False),
     (64, 12, 4, 300, 300, 0, 7, 2, False), (64, 2, 2, 64, 64, 0, 64, 0, False), (128, 32, 2, 65, 200, 133, 33, 31, False),
@@ -525,6 +554,26 @@ def test_paged_items_beyond_32_bits():
     """65535 sequences that may hold 65535 rows each, over 9 kv heads of 16: 2.4e9 pairs of row tiles."""
     O = _loose(BF, 64, 144, 9, [1] * 65535, [1 + i % 5 for i in range(65535)], [0, 1, 2, 30000, 65533, 65534])
     assert not bool((O == 7.0).flatten(1).all(1).any())
+
+
+@pytest.mark.parametrize("H,Hkv", [(5, 1), (7, 1), (6, 2), (22, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_items_of_groups_that_do_not_divide_a_tile(d, H, Hkv):
+    """Long items cut between CTAs and joined, rows of whole tokens that leave the end of a tile empty."""
+    _paged(BF, d, H, Hkv, [200, 1, 300, 90], [9000, 9000, 300, 5001], 64, 0, 0)
+    _paged(BF, d, H, Hkv, [200, 301], [9000, 6000], 16, 4000, 200)
+    _forward(BF, d, H, Hkv, 1, 100, 9100, 9101, 9000, 0, 0)
+
+
+def test_append_in_place():
+    """Q rotated in place: what a Q_out of its own gets."""
+    P = Pages(BF, 64, 6, 2, [30, 2], [100, 9], 16, pad=1)
+    r = hsa.make_rope(64)
+    K, V = P.K.clone(), P.V.clone()
+    want = hsa.paged_append(P.k, P.v, K, V, P.q_start, P.kv_len, P.table, Q=P.Q, rope=r, Q_out=P.Q.clone())
+    Q = P.Q.clone()
+    assert hsa.paged_append(P.k, P.v, P.K, P.V, P.q_start, P.kv_len, P.table, Q=Q, rope=r, Q_out=Q) is Q
+    assert torch.equal(Q, want) and torch.equal(P.K, K) and torch.equal(P.V, V)
 
 
 def test_paged_bad_pages_and_lengths():
