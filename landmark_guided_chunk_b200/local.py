@@ -9,7 +9,10 @@ window == 0, or p - u < window, or u < sinks.
 Same manner as the rest of the package: torch supplies device memory and the
 current stream, every step runs in the library's kernels.  The workspace's
 status word is sticky for these calls (device_status() reads and clears it);
-window_workspace and paged_workspace return one that starts clean.
+window_workspace and paged_workspace return one that starts clean.  It is the
+only place for what the kernels find: a page number or length outside its
+bounds, a wait that ran out.  A call that is given no workspace makes one for
+itself, which nobody can ask: give one wherever that matters.
 """
 from __future__ import annotations
 
@@ -203,8 +206,9 @@ def window_workspace(Q, K, window, sinks=0, q_pos0=0, kv_len=None, backward=Fals
 def window_attend(Q, K, V, window, sinks=0, q_pos0=0, kv_len=None, scale=None, O=None, ws=None, return_lse=False,
                   force_simt=False):
     """Sliding-window attention with sinks: Q [B,Tq,H,d] at positions q_pos0 .. over K, V [B,Tcap,Hkv,d], of which
-    the first kv_len tokens are cached (default: all).  window 0: every past key.  Returns O, or (O, lse) with
-    return_lse (lse [B,Tq,H] fp32, which window_backward takes).  Rows that see no key are zeros, lse -inf."""
+    the first kv_len tokens are cached (default: all).  window 0: every past key.  scale None or 0: 1 / sqrt(d).
+    Returns O, or (O, lse) with return_lse (lse [B,Tq,H] fp32, which window_backward takes).  Rows that see no key are
+    zeros, lse -inf.  Without ws a wait that ran out goes unreported (device_status(ws))."""
     _check(Q, K, V, O)
     _shape("V", V, K.shape)
     _shape("O", O, Q.shape)
@@ -221,7 +225,8 @@ def window_attend(Q, K, V, window, sinks=0, q_pos0=0, kv_len=None, scale=None, O
 def window_backward(Q, K, V, O, lse, dO, window, sinks=0, q_pos0=0, kv_len=None, scale=None, out=None, ws=None,
                     force_simt=False):
     """Gradients (dQ, dK, dV), in Q's dtype, of window_attend for the output gradient dO; O and lse as it
-    returned them.  out: optional preallocated (dQ, dK, dV), overwritten."""
+    returned them.  out: optional preallocated (dQ, dK, dV), overwritten.  Without ws a wait that ran out goes
+    unreported (device_status(ws))."""
     dQ, dK, dV = out if out is not None else (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
     _check(Q, K, V, O, dO, dQ, dK, dV)
     _shape("V", V, K.shape)
@@ -262,7 +267,8 @@ def paged_append(k_new, v_new, K_pages, V_pages, q_start, kv_len, table, Q=None,
     sequence b owns rows q_start[b] .. q_start[b+1] - 1 and kv_len[b] counts its cached tokens with them; token u
     lies in page table[b, u // page] (q_start [B+1], kv_len [B], table [B,max_pages] int32 on the device).  With
     rope (make_rope) K is rotated to its position on the way, and Q [rows,H,d] too.  Returns Q_out (Q rotated; a
-    new tensor unless given; rows behind the last sequence are not written), or None without Q."""
+    new tensor unless given; rows behind the last sequence are not written), or None without Q.  Without ws a page number
+    or length outside its bounds, whose write is skipped, goes unreported (device_status(ws))."""
     _check(k_new, v_new, K_pages, V_pages, Q, Q_out)
     _ints(k_new, q_start=q_start, kv_len=kv_len, table=table)
     rows, Hkv, d = k_new.shape
@@ -293,8 +299,10 @@ def paged_attend(Q, K_pages, V_pages, q_start, kv_len, table, max_q=None, max_kv
                  O=None, ws=None, force_simt=False):
     """Attention of the new tokens Q [rows,H,d] over the pages (which hold them already: paged_append first), with
     window and sinks as in window_attend.  max_q, max_kv: the most new and cached tokens of one sequence (defaults:
-    rows, and what a table row can hold); the closer they are, the better the work is split.  Returns O; rows
-    behind the last sequence are not written."""
+    rows, and what a table row can hold); the closer they are, the better the work is split.  scale None or 0:
+    1 / sqrt(d).  Returns O; rows behind the last sequence are not written.  Without ws a page number outside the pool
+    (zeros in its place), a length outside its bounds (cut to them) and a wait that ran out go unreported
+    (device_status(ws))."""
     _check(Q, K_pages, V_pages, O)
     _ints(Q, q_start=q_start, kv_len=kv_len, table=table)
     rows, H, d = Q.shape
