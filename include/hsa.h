@@ -354,12 +354,14 @@ HSA_API hsa_status_t hsa_backward(const hsa_problem_t *p, const void *Q, const v
  * Shared by these calls, beyond the conventions at the top:
  *   - Visibility: the query at position p sees key u iff u <= p, u is cached, and
  *     (window == 0, or p - u < window, or u < sinks).  A row that sees no key outputs zeros.
- *   - d in {64, 128}; H % Hkv == 0, G = H / Hkv <= 16; B <= 65535; positions below 2^30.
+ *   - d in {64, 128}; H % Hkv == 0, G = H / Hkv <= 16 (hsa_rope: any H, Hkv); B <= 65535; positions
+ *     below 2^30.
  *   - Values of keys that no query of the call sees (past the cached length, behind the window)
  *     may be anything, NaN included; they are never used.  Other inputs are assumed finite.
  *   - The status word at the start of the workspace is STICKY here: these calls never clear it (no
  *     extra launch in a decode step), they only add to it.  Zero the workspace's first 256 bytes
  *     once; hsa_get_device_status() reads and clears it and so reports on all calls since.
+ *   - Outputs overlap no other argument, except where a call says so.
  */
 typedef struct {
     int32_t B, Tq, Tkv, H, Hkv, d;

@@ -11,8 +11,8 @@
 // distributed shared memory (one launch, no workspace), or, for more splits than a
 // cluster holds, as partials that combine_kernel joins.
 //
-// 64 sequences of up to 16384 paged tokens, 32 + 8 heads of 128: 442 us, 5.7 TB/s (88% of
-// the measured copy rate); 8 sequences, window 4096: 27 us, 4.9 TB/s (256 CTAs on 148 SMs:
+// 64 sequences of up to 16384 paged tokens, 32 + 8 heads of 128: 450 us, 5.6 TB/s (86% of
+// the measured copy rate); 8 sequences, window 4096: 28.7 us, 4.7 TB/s (256 CTAs on 148 SMs:
 // the SMs with two set the time).  The tcgen05 kernel, whose tiles hold 128 rows: 862 and 57 us.
 #include "decode_mma.cuh"
 #include "local.cuh"
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(NT) window_few_kernel(const __grid_constant__ 
 }
 
 // D of the query rows that see few keys, for the backward: D = sum_u P[u] dP[u], P = exp(scale S - lse), dP = dO . V[u],
-// in fp32.  dO . O is the same in exact arithmetic, but the bf16 O is off by 2^-9 of itself, and over n equal keys that
+// in fp32.  dO . O is the same in exact arithmetic, but the bf16 O is off by up to 2^-8 of itself, and over n equal keys that
 // part of dQ and dK is about 1 / sqrt(n) of the one that rounding dS leaves: as large with one key, nothing with many.
 // A warp takes 16 rows (token, head of the group), keys in eights; 16-byte chunks go straight to the fragments (the
 // contraction runs over the elements in any order that both operands share).

@@ -17,11 +17,11 @@
 // softmax runs under the other's products.  P overwrites S in TMEM as bf16 and is
 // the A operand of PV from there.
 //
-// Bound: the softmax warps (two per SM sub-partition; a pair of tiles takes about 3400
-// cycles against 2080 for its products).  32 + 8 heads of 128, sinks 4: 65536 tokens,
-// window 4096: 3.83 ms, 1.11 PFLOP/s of visible pairs (66% of the measured 1.68); 16384
-// tokens: 0.90 ms; window 512: 0.226 ms (0.60 PFLOP/s: a fifth of its keys are masked and
-// an item's start and end cost four key tiles); head dim 64, window 4096: 0.83 ms.
+// Bound: the chain scores, softmax, product, next scores of a row tile.  A pair of tiles takes about 3400 cycles, its
+// products 2080; with no softmax arithmetic at all the loop still takes 781 of 890 us (16384 tokens, window 4096).
+// 32 + 8 heads of 128, sinks 4: 65536 tokens, window 4096: 4.4 ms among calls with new inputs, 0.97 PFLOP/s of visible
+// pairs (58% of the measured 1.68; 3.9 ms while the clock holds); 16384 tokens: 0.90 ms; window 512: 0.215 ms (a
+// fifth of its keys are masked and an item's start and end cost four key tiles); head dim 64, window 4096: 0.82 ms.
 #include <limits.h>
 
 #include "local.cuh"
