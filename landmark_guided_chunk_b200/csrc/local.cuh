@@ -181,7 +181,7 @@ struct LocPlan {
     bool tc, few;          // forward path: tcgen05 tiles, few-row kernel; neither: CUDA-core tiles
     int nsplit;
     size_t opart, lpart, starts;   // offsets; starts 0: no shares
-    size_t total;                  // enough for every call of smaller B, rows, max_q and max_kv too
+    size_t need, total;            // what this call uses; enough for every call of smaller B, rows, max_q and max_kv too
 };
 LocPlan plan_forward(const LocArgs &a, int dtype, bool simt);
 

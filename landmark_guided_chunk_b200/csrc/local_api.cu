@@ -120,7 +120,7 @@ hsa_status_t need4(const void *x, const char *name) {
 hsa_status_t run_forward(LocArgs &a, int dtype, unsigned flags, const void *Q, const void *K, const void *V, void *O,
                          void *ws, size_t ws_bytes, cudaStream_t st) {
     const LocPlan pl = plan_forward(a, dtype, (flags & HSA_FLAG_SIMT) != 0);
-    HSA_TRY(check_ws(pl.total, ws, ws_bytes));
+    HSA_TRY(check_ws(pl.need, ws, ws_bytes));
     if (a.B == 0 || a.rows == 0 || a.max_q == 0) return HSA_OK;
     a.status = (uint32_t *)ws;
     a.nsplit = pl.nsplit;
@@ -214,6 +214,7 @@ LocPlan plan_forward(const LocArgs &a, int dtype, bool simt) {
         p.lpart = off;
         off += align256(r * sizeof(float));
     }
+    p.need = off;
     const size_t most = HDR + forward_most(a, dtype, simt);
     p.total = off > most ? off : most;
     return p;

@@ -610,6 +610,17 @@ def test_paged_bad_pages_and_lengths():
     assert torch.equal(P.K, K0) and torch.equal(P.V, V0)
 
 
+def test_a_call_needs_no_more_than_it_uses():
+    """A prompt that is not split runs in the 256 bytes of the status word, whatever smaller ones would need."""
+    Q, K = _rand(1, BF, 4, 4100, 32, 64), _rand(2, BF, 4, 4100, 8, 64)
+    ws = hsa.window_workspace(Q, K, 0)
+    assert ws.numel() > 1 << 20
+    O = hsa.window_attend(Q, K, K, 0, ws=ws)
+    assert torch.equal(hsa.window_attend(Q, K, K, 0, ws=ws[:256].clone()), O)
+    with pytest.raises(hsa.HSAError):
+        hsa.window_attend(Q, K, K, 0, ws=ws[:255].clone())
+
+
 def test_workspaces_elsewhere_are_refused():
     P = Pages(BF, 64, 4, 2, [4, 1], [100, 40], 32)
     Q, K = _rand(1, BF, 1, 9, 4, 64), _rand(2, BF, 1, 9, 2, 64)
